@@ -22,14 +22,32 @@ Entry points (same names as the C ABI):
     kda_chunk_bwd_prologue(q_raw, k_raw, v, gate_pre, beta_pre, log_alpha_min, grad_o, ...)
     chunk_kda(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None)        (autograd: fwd + bwd)
     chunk_gated_delta_rule(q, k, v, log_alpha_or_None, beta, ...)       (autograd, scalar gate)
+    kda_chunk_bwd_act8(q8, k8, v8, log_alpha, beta, grad_o, ...)        (q, k, v saved in 8 bits)
+    kda_gdn_chunk_bwd_act8(q8, k8, v8, log_alpha_or_None, beta, grad_o, ...)
+    kda_glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, ...)             (gated linear recurrence)
+    kda_glr_bwd(log_alpha, h, grad_h, ...), kda_glr_bwd_act8(log_alpha, h_codes, h_scales, grad_h, ...)
+    kda_glr_step(x, log_alpha, S, h=None)
+    kda_act8_pack(x), kda_act8_unpack(codes, scales, dtype)              (8-bit activation checkpoints)
+    kda_rmsnorm_fwd(x, weight, residual, eps), kda_rmsnorm_fwd_act8(...)
+    kda_rmsnorm_bwd(r, weight, rstd, grad_y, grad_r), kda_rmsnorm_bwd_act8(r_codes, r_scales, ...)
+    gated_linear_recurrence(x, log_alpha, ...), rms_norm(x, weight, residual, ...)   (autograd)
     kda_chunk_fwd_workspace_size(...), kda_chunk_bwd_workspace_size(...),
     kda_gdn_chunk_bwd_workspace_size(...),
     kda_status_string(code), kda_abi_version()
+
+chunk_kda, chunk_gated_delta_rule, gated_linear_recurrence and rms_norm take
+act8=True to keep what the backward reads in 8 bits.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+
+from . import ops as _ops
+from .ops import (gated_linear_recurrence, kda_act8_pack, kda_act8_unpack, kda_chunk_bwd_act8,
+                  kda_chunk_bwd_act8_workspace_size, kda_gdn_chunk_bwd_act8, kda_glr_bwd, kda_glr_bwd_act8,
+                  kda_glr_fwd, kda_glr_step, kda_glr_workspace_size, kda_rmsnorm_bwd, kda_rmsnorm_bwd_act8,
+                  kda_rmsnorm_bwd_workspace_size, kda_rmsnorm_fwd, kda_rmsnorm_fwd_act8, rms_norm)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -43,7 +61,7 @@ EXPORTED_SYMBOLS = ("kda_abi_version", "kda_status_string", "kda_last_hip_error"
                     "kda_chunk_bwd_workspace_size", "kda_chunk_bwd",
                     "kda_gdn_chunk_bwd_workspace_size", "kda_gdn_chunk_bwd", "kda_chunk_bwd_decoupled",
                     "kda_chunk_bwd_prologue_workspace_size", "kda_chunk_bwd_prologue",
-                    "kda_chunk_fwd_noalloc")
+                    "kda_chunk_fwd_noalloc") + _ops.SYMBOLS
 
 _lib = None
 
@@ -117,6 +135,7 @@ def load_library(path: str = LIB_PATH):
     lib.kda_chunk_bwd_prologue.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                            vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, ctypes.c_int, vp, sz, vp]
     lib.kda_chunk_bwd_prologue.restype = ctypes.c_int
+    _ops.declare(lib)
     _lib = lib
     return lib
 
@@ -548,23 +567,32 @@ def _autograd_function():
 
     class _ChunkKDA(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, v, log_alpha, beta, h0, cu_seqlens, gdn):
+        def forward(ctx, q, k, v, log_alpha, beta, h0, cu_seqlens, gdn, act8):
             fwd = kda_gdn_chunk_fwd if gdn else kda_chunk_fwd
             o, h_T = fwd(q, k, v, log_alpha, beta, h0=h0, cu_seqlens=cu_seqlens)
-            ctx.save_for_backward(q, k, v, log_alpha, beta, h0, cu_seqlens)
-            ctx.gdn = gdn
+            if act8:
+                saved = kda_act8_pack(q) + kda_act8_pack(k) + kda_act8_pack(v)
+            else:
+                saved = (q, k, v)
+            ctx.save_for_backward(log_alpha, beta, h0, cu_seqlens, *saved)
+            ctx.gdn, ctx.act8 = gdn, act8
             return o, h_T
 
         @staticmethod
         def backward(ctx, grad_o, grad_hT):
-            q, k, v, log_alpha, beta, h0, cu_seqlens = ctx.saved_tensors
-            if grad_o is None:
-                grad_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
-            bwd = kda_gdn_chunk_bwd if ctx.gdn else kda_chunk_bwd
-            dq, dk, dv, dla, db, dh0 = bwd(q, k, v, log_alpha, beta, grad_o.contiguous(), h0=h0,
+            log_alpha, beta, h0, cu_seqlens, *saved = ctx.saved_tensors
+            if ctx.act8:
+                saved = saved[0:2], saved[2:4], saved[4:6]
+                bwd = kda_gdn_chunk_bwd_act8 if ctx.gdn else kda_chunk_bwd_act8
+            else:
+                v = saved[2]
+                if grad_o is None:
+                    grad_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+                bwd = kda_gdn_chunk_bwd if ctx.gdn else kda_chunk_bwd
+            dq, dk, dv, dla, db, dh0 = bwd(*saved, log_alpha, beta, grad_o.contiguous(), h0=h0,
                                            grad_hT=None if grad_hT is None else grad_hT.contiguous(),
                                            cu_seqlens=cu_seqlens, want_grad_h0=h0 is not None and ctx.needs_input_grad[5])
-            return dq, dk, dv, dla, db, dh0, None, None
+            return dq, dk, dv, dla, db, dh0, None, None, None
 
     return _ChunkKDA
 
@@ -572,19 +600,22 @@ def _autograd_function():
 _CHUNK_KDA = None
 
 
-def chunk_kda(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None):
+def chunk_kda(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None, *, act8=False):
     """KDA prefill with autograd: returns (o, h_T) as kda_chunk_fwd does, and
-    gradients flow to q, k, v, log_alpha, beta and h0 through kda_chunk_bwd."""
+    gradients flow to q, k, v, log_alpha, beta and h0 through kda_chunk_bwd.  With
+    act8 the forward keeps q, k and v for the backward in 8 bits (about half of
+    bf16's memory) and the gradients are those at the values these stand for."""
     global _CHUNK_KDA
     if _CHUNK_KDA is None:
         _CHUNK_KDA = _autograd_function()
-    return _CHUNK_KDA.apply(q, k, v, log_alpha, beta, h0, cu_seqlens, False)
+    return _CHUNK_KDA.apply(q, k, v, log_alpha, beta, h0, cu_seqlens, False, act8)
 
 
-def chunk_gated_delta_rule(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None):
+def chunk_gated_delta_rule(q, k, v, log_alpha, beta, h0=None, cu_seqlens=None, *, act8=False):
     """Gated DeltaNet (log_alpha [.., H]) or DeltaNet (log_alpha None) prefill
-    with autograd, through kda_gdn_chunk_fwd and kda_gdn_chunk_bwd."""
+    with autograd, through kda_gdn_chunk_fwd and kda_gdn_chunk_bwd; act8 as for
+    chunk_kda."""
     global _CHUNK_KDA
     if _CHUNK_KDA is None:
         _CHUNK_KDA = _autograd_function()
-    return _CHUNK_KDA.apply(q, k, v, log_alpha, beta, h0, cu_seqlens, True)
+    return _CHUNK_KDA.apply(q, k, v, log_alpha, beta, h0, cu_seqlens, True, act8)

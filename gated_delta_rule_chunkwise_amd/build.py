@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_chunk.hip", "kda_chunk2.hip", "kda_fused.hip", "kda_decode.hip", "kda_bwd.hip",
-           "kda_noalloc.hip"]
+           "kda_noalloc.hip", "kda_ops_api.cpp", "kda_glr.hip", "kda_act8.hip", "kda_norm.hip"]
 
 # The packed fp32 VALU forms are switched off for the device code, which is
 # written with scalar or float2 arithmetic only; hipcc's host pass warns that it

@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "kda_launch.h"
+#include "kda_ops_launch.h"
 
 namespace {
 
@@ -44,6 +45,13 @@ kda_status_t decode_step_impl(const void *q, const void *k, const void *v, const
                               bool prologue, float lo, int gate_mode);
 
 }  // namespace
+
+namespace kda {
+char *hip_error_text(size_t *len) {
+    *len = sizeof(g_hip_error);
+    return g_hip_error;
+}
+}  // namespace kda
 
 extern "C" {
 

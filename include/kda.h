@@ -460,6 +460,225 @@ kda_status_t kda_gdn_chunk_bwd(const void *q, const void *k, const void *v, cons
                                int32_t gate_dtype, void *workspace, size_t workspace_bytes,
                                void *stream);
 
+/* ------------------------------------------------------------------------------
+ * Gated linear recurrence, 8-bit activation checkpoints and RMS norm.
+ *
+ * The calls below follow the conventions at the top of this file, except that
+ * their tensors need only the alignment of their elements (wider loads are used
+ * where the base pointers allow them).
+ */
+
+/*
+ * Bytes of device workspace kda_glr_fwd, kda_glr_bwd and kda_glr_bwd_act8 need
+ * (0 if none, or for invalid arguments).  A batch of at most 1024 tokens in
+ * all, or one of many short equal-length sequences, needs none; other batches
+ * keep, per time tile and channel, the tile's composed map and, per group of
+ * tiles, the state behind it (about 0.1 bytes per token and channel).  The size
+ * depends only on the arguments.
+ */
+size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs, int32_t io_dtype);
+
+/*
+ * kda_glr_fwd -- gated linear recurrence over a batch of sequences: the diagonal
+ * member of the family, one fp32 state per channel.  For each sequence, channel
+ * and token t
+ *
+ *     h_t = alpha_t h_{t-1} + x_t,      alpha_t = exp(log_alpha_t)
+ *
+ *   x           [B, T, D]  io_dtype
+ *   log_alpha   [B, T, D]  gate_dtype; <= 0, finite or -inf.  alpha_t = 0 (-inf,
+ *               or a value whose exponential underflows) is a reset: h_t = x_t
+ *               whatever came before, also where that is infinite or NaN.
+ *   h0          [N, D] fp32 initial state per sequence, or NULL (zeros)
+ *   cu_seqlens  device int32 [N+1] or NULL, as for kda_chunk_fwd
+ *   h           [B, T, D]  io_dtype (out)
+ *   h_T         [N, D] fp32 final state per sequence (out), or NULL; may alias
+ *               h0 exactly.  A zero-length sequence gives h_T = h0 (or zeros).
+ *   D           any size >= 1
+ *   workspace   device scratch of at least kda_glr_workspace_size() bytes (may be
+ *               NULL when that size is 0), 16-byte aligned, owned by the caller;
+ *               its contents on entry do not matter.  Two calls in flight at once
+ *               on different streams must not share one workspace.
+ *
+ * Numerics: states and every product are fp32; h is rounded to io_dtype with
+ * round-to-nearest-even.  Deterministic: the same inputs give bitwise identical
+ * outputs.  The products of decays over a span of tokens are formed in fp32; a
+ * span whose product underflows counts as a reset.
+ */
+kda_status_t kda_glr_fwd(const void *x, const void *log_alpha, const float *h0, const int32_t *cu_seqlens,
+                         int32_t num_seqs, void *h, float *h_T, int32_t B, int32_t T, int32_t D, int32_t io_dtype,
+                         int32_t gate_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_glr_bwd -- gradients of kda_glr_fwd.  With grad_h, grad_hT the gradients
+ * of a loss with respect to h and h_T, and c behind a sequence's last token
+ * equal to grad_hT (or 0), for t from last to first:
+ *
+ *     g_t = grad_h_t + c_{t+1},   c_t = alpha_t g_t,
+ *     grad_x_t = g_t,   grad_log_alpha_t = h_{t-1} c_t,   grad_h0 = c_1
+ *
+ *   log_alpha, h0, cu_seqlens, num_seqs, B, T, D, io_dtype, gate_dtype,
+ *   workspace       the forward's, as for kda_glr_fwd
+ *   h               [B, T, D]  io_dtype: the forward's output.  grad_log_alpha is
+ *                   that of these values (h rounded to io_dtype).
+ *   grad_h          [B, T, D]  io_dtype
+ *   grad_hT         [N, D] fp32, or NULL
+ *   grad_x          [B, T, D]  io_dtype (out)
+ *   grad_log_alpha  [B, T, D]  gate_dtype (out); 0 at a reset
+ *   grad_h0         [N, D] fp32 (out), or NULL; given also when h0 is NULL.  A
+ *                   zero-length sequence gives grad_h0 = grad_hT (or zeros).
+ */
+kda_status_t kda_glr_bwd(const void *log_alpha, const void *h, const float *h0, const int32_t *cu_seqlens,
+                         int32_t num_seqs, const void *grad_h, const float *grad_hT, void *grad_x,
+                         void *grad_log_alpha, float *grad_h0, int32_t B, int32_t T, int32_t D, int32_t io_dtype,
+                         int32_t gate_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_glr_bwd_act8 -- kda_glr_bwd with h taken from its 8-bit checkpoint:
+ * h_codes [B, T, D] int8 and h_scales [B, T, ceil(D / 128)] fp32 as kda_act8_pack
+ * writes them for h.  Only grad_log_alpha reads h, linearly.
+ */
+kda_status_t kda_glr_bwd_act8(const void *log_alpha, const int8_t *h_codes, const float *h_scales, const float *h0,
+                              const int32_t *cu_seqlens, int32_t num_seqs, const void *grad_h, const float *grad_hT,
+                              void *grad_x, void *grad_log_alpha, float *grad_h0, int32_t B, int32_t T, int32_t D,
+                              int32_t io_dtype, int32_t gate_dtype, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * kda_glr_step -- one token of kda_glr_fwd for B resident states (decode):
+ * S <- alpha S + x in place, h = S rounded to io_dtype.
+ *
+ *   x [B, D] io_dtype; log_alpha [B, D] gate_dtype; S [B, D] fp32, read and
+ *   overwritten; h [B, D] io_dtype (out)
+ */
+kda_status_t kda_glr_step(const void *x, const void *log_alpha, float *S, void *h, int32_t B, int32_t D,
+                          int32_t io_dtype, int32_t gate_dtype, void *stream);
+
+/*
+ * kda_act8_pack -- an activation saved for the backward pass in 8 bits.  Each
+ * block of 128 consecutive values of a row (the last block of a row may be
+ * shorter) is held as whole numbers -127..127 and one fp32 scale:
+ *
+ *     scale = max(max|x| / 127, 2^-126),   code = x / scale rounded to nearest
+ *
+ * (ties of the exact quotient to the even code), so that code * scale is within
+ * scale / 2 of x.  A block that holds an infinity or a NaN gets a NaN scale and
+ * codes 0: it reads back as NaN throughout.
+ *
+ *   x       [rows, cols]  io_dtype
+ *   codes   [rows, cols]  int8 (out)
+ *   scales  [rows, ceil(cols / 128)]  fp32 (out)
+ *
+ * rows may be 0.  An activation [.., H, d] is packed with rows the product of
+ * the leading axes and cols = d: one scale per (token, head).
+ */
+kda_status_t kda_act8_pack(const void *x, int8_t *codes, float *scales, int64_t rows, int32_t cols, int32_t io_dtype,
+                           void *stream);
+
+/* kda_act8_unpack -- x = code * scale, rounded to io_dtype (x [rows, cols], out). */
+kda_status_t kda_act8_unpack(const int8_t *codes, const float *scales, void *x, int64_t rows, int32_t cols,
+                             int32_t io_dtype, void *stream);
+
+/*
+ * kda_chunk_bwd_act8 -- kda_chunk_bwd with q, k and v taken from their 8-bit
+ * checkpoints (codes and scales as kda_act8_pack writes them for [B, T, H, d]:
+ * codes [B, T, H, d] int8, scales [B, T, H] fp32).  The codes are read back into
+ * io_dtype in the workspace and the gradients of kda_chunk_bwd are taken at those
+ * values.  The gates are not held in 8 bits: their errors would compound over a
+ * sequence.  Other arguments, outputs and errors as for kda_chunk_bwd; the
+ * workspace is kda_chunk_bwd_act8_workspace_size() bytes.
+ */
+size_t kda_chunk_bwd_act8_workspace_size(int32_t B, int32_t T, int32_t H, int32_t d_k, int32_t d_v,
+                                         int32_t num_seqs, int32_t io_dtype);
+kda_status_t kda_chunk_bwd_act8(const int8_t *q_codes, const float *q_scales, const int8_t *k_codes,
+                                const float *k_scales, const int8_t *v_codes, const float *v_scales,
+                                const void *log_alpha, const void *beta, const float *h0, const int32_t *cu_seqlens,
+                                int32_t num_seqs, const void *grad_o, const float *grad_hT, void *grad_q,
+                                void *grad_k, void *grad_v, void *grad_log_alpha, void *grad_beta, float *grad_h0,
+                                int32_t B, int32_t T, int32_t H, int32_t d_k, int32_t d_v, int32_t io_dtype,
+                                int32_t gate_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_gdn_chunk_bwd_act8 -- the same for kda_gdn_chunk_bwd (scalar gates, or none
+ * when log_alpha is NULL), with the same workspace.
+ */
+kda_status_t kda_gdn_chunk_bwd_act8(const int8_t *q_codes, const float *q_scales, const int8_t *k_codes,
+                                    const float *k_scales, const int8_t *v_codes, const float *v_scales,
+                                    const void *log_alpha, const void *beta, const float *h0,
+                                    const int32_t *cu_seqlens, int32_t num_seqs, const void *grad_o,
+                                    const float *grad_hT, void *grad_q, void *grad_k, void *grad_v,
+                                    void *grad_log_alpha, void *grad_beta, float *grad_h0, int32_t B, int32_t T,
+                                    int32_t H, int32_t d_k, int32_t d_v, int32_t io_dtype, int32_t gate_dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_rmsnorm_fwd -- root-mean-square norm of a row, with the residual stream's
+ * addition:
+ *
+ *     r = x + residual (rounded to io_dtype),   rstd = 1 / sqrt(mean(r^2) + eps),
+ *     y = r rstd weight
+ *
+ *   x         [rows, cols] io_dtype
+ *   residual  [rows, cols] io_dtype, or NULL (r = x)
+ *   weight    [cols] w_dtype, or NULL (ones)
+ *   y         [rows, cols] io_dtype (out)
+ *   r         [rows, cols] io_dtype (out): the new residual stream; required with
+ *             a residual, ignored without one.  May alias x or residual exactly.
+ *   rstd      [rows] fp32 (out) for the backward, or NULL
+ *   eps       finite and > 0
+ *
+ * rows may be 0.  The mixers' per-head output norm is the same call on rows of
+ * cols = d_v.  Numerics: the mean and every product are fp32, in a fixed order.
+ */
+kda_status_t kda_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *y, void *r, float *rstd,
+                             int64_t rows, int32_t cols, float eps, int32_t io_dtype, int32_t w_dtype, void *stream);
+
+/*
+ * kda_rmsnorm_fwd_act8 -- kda_rmsnorm_fwd with y in 8 bits: codes [rows, cols] and
+ * scales [rows, ceil(cols / 128)] as kda_act8_pack would write them for y, taken
+ * from the fp32 values of y (y itself is not written).
+ */
+kda_status_t kda_rmsnorm_fwd_act8(const void *x, const void *residual, const void *weight, int8_t *codes,
+                                  float *scales, void *r, float *rstd, int64_t rows, int32_t cols, float eps,
+                                  int32_t io_dtype, int32_t w_dtype, void *stream);
+
+/* Bytes of device workspace kda_rmsnorm_bwd needs when grad_weight is wanted. */
+size_t kda_rmsnorm_bwd_workspace_size(int64_t rows, int32_t cols);
+
+/*
+ * kda_rmsnorm_bwd -- gradients of kda_rmsnorm_fwd.  With m the row's mean of
+ * r weight grad_y:
+ *
+ *     grad_x = rstd (weight grad_y - r rstd^2 m) + grad_r,
+ *     grad_weight = sum over rows of grad_y r rstd
+ *
+ *   r, rstd      the forward's (r is x where there was no residual)
+ *   grad_y       [rows, cols] io_dtype
+ *   grad_r       [rows, cols] io_dtype: the gradient that reaches the new residual
+ *                stream by its other uses, or NULL (none)
+ *   grad_x       [rows, cols] io_dtype (out): the gradient of x and of residual
+ *                alike.  May alias grad_r or grad_y exactly.
+ *   grad_weight  [cols] w_dtype (out), or NULL (not wanted); given also when weight
+ *                is NULL.  Zeros when rows is 0.
+ *   workspace    at least kda_rmsnorm_bwd_workspace_size() bytes, 16-byte aligned;
+ *                may be NULL when grad_weight is NULL or rows is 0
+ *
+ * Deterministic: the sum over rows is taken in a fixed order, in fp32.
+ */
+kda_status_t kda_rmsnorm_bwd(const void *r, const void *weight, const float *rstd, const void *grad_y,
+                             const void *grad_r, void *grad_x, void *grad_weight, int64_t rows, int32_t cols,
+                             int32_t io_dtype, int32_t w_dtype, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * kda_rmsnorm_bwd_act8 -- kda_rmsnorm_bwd with r taken from its 8-bit checkpoint
+ * (r_codes, r_scales as kda_act8_pack writes them for r).
+ */
+kda_status_t kda_rmsnorm_bwd_act8(const int8_t *r_codes, const float *r_scales, const void *weight, const float *rstd,
+                                  const void *grad_y, const void *grad_r, void *grad_x, void *grad_weight,
+                                  int64_t rows, int32_t cols, int32_t io_dtype, int32_t w_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
