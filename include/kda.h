@@ -470,10 +470,9 @@ kda_status_t kda_gdn_chunk_bwd(const void *q, const void *k, const void *v, cons
 
 /*
  * Bytes of device workspace kda_glr_fwd, kda_glr_bwd and kda_glr_bwd_act8 need
- * (0 if none, or for invalid arguments).  A batch of at most 1024 tokens in
- * all, or one of many short equal-length sequences, needs none; other batches
- * keep, per time tile and channel, the tile's composed map and, per group of
- * tiles, the state behind it (about 0.1 bytes per token and channel).  The size
+ * (0 if none, or for invalid arguments).  A batch of few tokens (one time tile)
+ * needs none; others keep one 8-byte map per time tile and channel (with
+ * many channels 1/16 byte per token and channel in bf16, 1/8 in fp32).  The size
  * depends only on the arguments.
  */
 size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs, int32_t io_dtype);
