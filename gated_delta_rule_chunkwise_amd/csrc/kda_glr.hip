@@ -39,6 +39,7 @@ constexpr int kW = 8;              // waves of a workgroup
 constexpr int kNT = 64 * kW;       // its threads
 constexpr int kG = 16;             // tiles of a group
 constexpr int kMinLanes = 8;       // channel lanes of a row at least
+constexpr int kTicketPitch = 32;   // a cache line of its own for each
 constexpr uint64_t kAbsent = ~(uint64_t)0;
 // A wait that could only be broken by a fault elsewhere still ends (after seconds),
 // with a NaN state.
@@ -46,15 +47,14 @@ constexpr int kMaxPolls = 1 << 24;
 
 enum Mode : int { kFwd = 0, kBwd = 1, kBwd8 = 2 };
 
-// Tokens of a row's span: what two (three) inputs take of the registers.
-template <typename IO> constexpr int span_tokens() { return sizeof(IO) == 2 ? 16 : 8; }
+constexpr int R = 32;              // tokens of a row's span
 
 // VEC consecutive values of X as loaded, and as fp32.
 template <typename X, int VEC> struct Raw;
 template <typename X> struct Raw<X, 1> { typedef X type; };
-template <> struct Raw<float, 4> { typedef f32x4_t type; };
-template <> struct Raw<bf16_t, 4> { typedef bf16x4_t type; };
-template <> struct Raw<int8_t, 4> { typedef int8_t type __attribute__((ext_vector_type(4))); };
+template <> struct Raw<float, 2> { typedef float type __attribute__((ext_vector_type(2))); };
+template <> struct Raw<bf16_t, 2> { typedef bf16x2_t type; };
+template <> struct Raw<int8_t, 2> { typedef int8_t type __attribute__((ext_vector_type(2))); };
 
 template <int VEC, typename RAW> __device__ __forceinline__ float raw_at(const RAW &r, int e) {
     if constexpr (VEC == 1) return (float)r;
@@ -91,7 +91,7 @@ struct GlrParams {
     int32_t D, chan_tiles, lane_log;   // lanes of a row: 1 << lane_log
     int64_t time_tiles;
     uint64_t *words;                   // [time_tiles, D] published maps
-    uint32_t *ticket;
+    uint32_t *tickets;                 // one for each channel tile, kTicketPitch apart
 };
 
 // The sequences of the flat token axis.
@@ -113,20 +113,18 @@ struct Seqs {
     }
 };
 
-template <typename IO, typename GT, int MODE, int VEC, int R> struct Row {
-    static constexpr bool kBack = MODE != kFwd;
+template <typename IO, typename GT, int MODE, int VEC> struct Row {
     typedef typename std::conditional<MODE == kBwd8, int8_t, IO>::type HT;
     typename Raw<IO, VEC>::type x[R];
     typename Raw<GT, VEC>::type la[R];
     typename Raw<HT, VEC>::type h[R];        // backward: h of the token before
-    float hs[MODE == kBwd8 ? R : 1];
     float start[VEC];                        // forward: h0 of the last sequence that starts here
     int start_at;
 };
 
 // ---- the span of one row, all of it inside one sequence ------------------------
-template <typename IO, typename GT, int MODE, int VEC, int R>
-__device__ __forceinline__ void compose_inside(const Row<IO, GT, MODE, VEC, R> &row, float (&L)[VEC], float (&B)[VEC]) {
+template <typename IO, typename GT, int MODE, int VEC>
+__device__ __forceinline__ void compose_inside(const Row<IO, GT, MODE, VEC> &row, float (&L)[VEC], float (&B)[VEC]) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int i = MODE == kFwd ? k : R - 1 - k;
@@ -139,9 +137,9 @@ __device__ __forceinline__ void compose_inside(const Row<IO, GT, MODE, VEC, R> &
     }
 }
 
-template <typename IO, typename GT, int MODE, int VEC, int R>
-__device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, GT, MODE, VEC, R> &row, int64_t t0,
-                                              int c0, float (&s)[VEC]) {
+template <typename IO, typename GT, int MODE, int VEC>
+__device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, GT, MODE, VEC> &row, const float *hs,
+                                              int64_t t0, int c0, float (&s)[VEC]) {
     IO *out = static_cast<IO *>(p.out);
     GT *dla = static_cast<GT *>(p.dla);
 #pragma unroll
@@ -159,7 +157,7 @@ __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, 
                 o[e] = x + s[e];
                 s[e] = decayed(a, o[e]);
                 float h = raw_at<VEC>(row.h[i], e);
-                if constexpr (MODE == kBwd8) h *= row.hs[i];
+                if constexpr (MODE == kBwd8) h *= hs[i];
                 d[e] = a == 0.f ? 0.f : h * s[e];
             }
         }
@@ -172,8 +170,8 @@ __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, 
 // A sequence that starts in one row and ends in another has its h0 read here, in
 // the first pass, and kept: its h_T, which may be the same memory, is written by
 // another workgroup as soon as this one has published.
-template <typename IO, typename GT, int MODE, int VEC, int R>
-__device__ __forceinline__ void compose_border(const GlrParams &p, const Seqs &q, Row<IO, GT, MODE, VEC, R> &row,
+template <typename IO, typename GT, int MODE, int VEC>
+__device__ __forceinline__ void compose_border(const GlrParams &p, const Seqs &q, Row<IO, GT, MODE, VEC> &row,
                                                int64_t t0, int nv, int c0, float (&L)[VEC], float (&B)[VEC]) {
     row.start_at = -1;
     if (nv <= 0) return;
@@ -214,9 +212,9 @@ __device__ __forceinline__ void compose_border(const GlrParams &p, const Seqs &q
     }
 }
 
-template <typename IO, typename GT, int MODE, int VEC, int R>
-__device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q, const Row<IO, GT, MODE, VEC, R> &row,
-                                              int64_t t0, int nv, int c0, float (&s)[VEC]) {
+template <typename IO, typename GT, int MODE, int VEC>
+__device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q, const Row<IO, GT, MODE, VEC> &row,
+                                              const float *hs, int64_t t0, int nv, int c0, float (&s)[VEC]) {
     if (nv <= 0) return;
     IO *out = static_cast<IO *>(p.out);
     GT *dla = static_cast<GT *>(p.dla);
@@ -243,7 +241,7 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 h[e] = raw_at<VEC>(row.h[i], e);
-                if constexpr (MODE == kBwd8) h[e] *= row.hs[i];
+                if constexpr (MODE == kBwd8) h[e] *= hs[i];
             }
             if (t == b) {
 #pragma unroll
@@ -285,27 +283,27 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
     }
 }
 
-template <int VEC> struct alignas(16) GlrShared {
+template <int MODE, int VEC> struct alignas(16) GlrShared {
     float A[kNT * VEC], B[kNT * VEC];               // the rows' maps
     float pA[kG][64 * VEC], pB[kG][64 * VEC];       // the published maps in front of the tile
+    float hs[MODE == kBwd8 ? kNT / kMinLanes * R : 1];   // scales of the rows' saved h
     uint32_t tile;
 };
 
 template <typename IO, typename GT, int MODE, int VEC>
 __global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
-    constexpr int R = span_tokens<IO>();
-    typedef typename Row<IO, GT, MODE, VEC, R>::HT HT;
-    __shared__ GlrShared<VEC> sm;
+    typedef typename Row<IO, GT, MODE, VEC>::HT HT;
+    __shared__ GlrShared<MODE, VEC> sm;
     const int tid = threadIdx.x;
-    int64_t tile = blockIdx.x;
+    const int ct = (int)(blockIdx.x % p.chan_tiles);
+    int64_t tt = 0;                                    // in the order of the scan
     if (p.time_tiles > 1) {
         if (tid == 0)
-            sm.tile = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            sm.tile = __hip_atomic_fetch_add(p.tickets + ct * kTicketPitch, 1u, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
-        tile = sm.tile;
+        tt = sm.tile;
     }
-    const int64_t tt = tile / p.chan_tiles;            // in the order of the scan
-    const int ct = (int)(tile % p.chan_tiles);
     const int lanes = 1 << p.lane_log, rows = kNT >> p.lane_log;
     const int cl = tid & (lanes - 1), v = tid >> p.lane_log;   // lane of a row, row in the order of the scan
     const int c0 = (ct * lanes + cl) * VEC;
@@ -317,7 +315,7 @@ __global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
     const int64_t t0 = span * R;
     const int nv = chan ? (int)max((int64_t)0, min((int64_t)R, valid - t0)) : 0;
 
-    Row<IO, GT, MODE, VEC, R> row;
+    Row<IO, GT, MODE, VEC> row;
     {
         const IO *x = static_cast<const IO *>(p.x) + t0 * p.D + c0;
         const GT *la = static_cast<const GT *>(p.la) + t0 * p.D + c0;
@@ -349,9 +347,9 @@ __global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) L[e] = 0.f, B[e] = 0.f;
     if (plain) {
-        if (chan) compose_inside<IO, GT, MODE, VEC, R>(row, L, B);
+        if (chan) compose_inside<IO, GT, MODE, VEC>(row, L, B);
     } else {
-        compose_border<IO, GT, MODE, VEC, R>(p, q, row, t0, nv, c0, L, B);
+        compose_border<IO, GT, MODE, VEC>(p, q, row, t0, nv, c0, L, B);
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -366,7 +364,13 @@ __global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
         for (int i = 0; i < R; ++i) {
             if (i < nv && t0 + i > 0) {
                 row.h[i] = load_raw<HT, VEC>(h + (int64_t)i * p.D);
-                if constexpr (MODE == kBwd8) row.hs[i] = p.hs[(t0 + i - 1) * nb + c0 / kAct8Block];
+            }
+        }
+        if constexpr (MODE == kBwd8) {   // a tile's channels lie in one block of 128
+            const int64_t tile0 = (p.time_tiles - 1 - tt) * rows * R;
+            for (int i = tid; i < rows * R; i += kNT) {
+                const int64_t t = tile0 + i;
+                if (t > 0 && t < valid) sm.hs[i] = p.hs[(t - 1) * nb + ct * lanes * VEC / kAct8Block];
             }
         }
     }
@@ -441,17 +445,18 @@ __global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
             s[e] = decayed(sm.A[k], s[e]) + sm.B[k];
         }
     }
+    const float *hs = sm.hs + (MODE == kBwd8 ? (rows - 1 - v) * R : 0);
     if (plain) {
-        if (chan) finish_inside<IO, GT, MODE, VEC, R>(p, row, t0, c0, s);
+        if (chan) finish_inside<IO, GT, MODE, VEC>(p, row, hs, t0, c0, s);
     } else {
-        finish_border<IO, GT, MODE, VEC, R>(p, q, row, t0, nv, c0, s);
+        finish_border<IO, GT, MODE, VEC>(p, q, row, hs, t0, nv, c0, s);
     }
 }
 
-// The workspace of a call: the ticket 0, every word absent.
-__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t *ticket, uint64_t *words, int64_t n) {
+// The workspace of a call: the tickets 0, every word absent.
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint32_t *tickets, int64_t nt, uint64_t *words, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i == 0) *ticket = 0;
+    for (int64_t k = i; k < nt; k += (int64_t)gridDim.x * 256) tickets[k] = 0;
     for (int64_t k = i; k < n; k += (int64_t)gridDim.x * 256) words[k] = kAbsent;
 }
 
@@ -472,9 +477,9 @@ struct GlrPlan {
     int vec, lane_log;
     int64_t chan_tiles, time_tiles;
 };
-// Four channels a lane where the addresses allow it, one otherwise.  A row of lanes
-// covers the channels up to a wave's width; with fewer channels a wave takes
-// several rows.
+// Two channels a lane in bf16 where the addresses allow it, one otherwise: a wave's
+// load is 256 bytes of a token (128 in the odd bf16 case).  A row of lanes covers
+// the channels up to a wave's width; with fewer channels a wave takes several rows.
 GlrPlan glr_plan(const GlrArgs &a, int vec) {
     GlrPlan g = {};
     g.vec = vec;
@@ -482,7 +487,7 @@ GlrPlan glr_plan(const GlrArgs &a, int vec) {
     g.lane_log = 3;
     while (g.lane_log < 6 && (1 << g.lane_log) < need) ++g.lane_log;
     g.chan_tiles = ceil_div(need, (int64_t)1 << g.lane_log);
-    const int64_t tile = (int64_t)(kNT >> g.lane_log) * (a.io_bf16 ? span_tokens<bf16_t>() : span_tokens<float>());
+    const int64_t tile = (int64_t)(kNT >> g.lane_log) * R;
     g.time_tiles = a.tokens > tile ? ceil_div(a.tokens, tile) : 1;
     return g;
 }
@@ -490,26 +495,31 @@ static_assert(kMinLanes == 8, "the plan's smallest row");
 
 bool glr_aligned(const GlrArgs &a) {
     const auto ok = [](const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
-    const uintptr_t io = a.io_bf16 ? 8 : 16, gt = a.gate_bf16 ? 8 : 16;
-    return a.D % 4 == 0 && ok(a.x, io) && ok(a.out, io) && ok(a.log_alpha, gt) && ok(a.dlog_alpha, gt) &&
-           ok(a.h_in, a.h_scales ? 4 : io);
+    const uintptr_t gt = a.gate_bf16 ? 4 : 8;
+    return a.D % 2 == 0 && ok(a.x, 4) && ok(a.out, 4) && ok(a.log_alpha, gt) && ok(a.dlog_alpha, gt) &&
+           ok(a.h_in, a.h_scales ? 2 : 4);
 }
 
 template <typename IO, typename GT, int MODE> hipError_t launch_m(const GlrArgs &a, hipStream_t st) {
-    const GlrPlan g = glr_plan(a, glr_aligned(a) ? 4 : 1);
+    const GlrPlan g = glr_plan(a, a.io_bf16 && glr_aligned(a) ? 2 : 1);
     GlrParams p = {a.x, a.log_alpha, a.h_in, a.h_scales, a.h0, a.d_hT, a.cu_seqlens, a.out, a.dlog_alpha, a.state_out,
                    a.num_seqs, a.seq_len, a.tokens, a.D, (int32_t)g.chan_tiles, g.lane_log, g.time_tiles, nullptr,
                    nullptr};
     if (g.time_tiles > 1) {
-        p.ticket = static_cast<uint32_t *>(a.workspace);
-        p.words = reinterpret_cast<uint64_t *>(static_cast<uint8_t *>(a.workspace) + 256);
-        const int64_t n = g.time_tiles * a.D;
+        const int64_t nt = g.chan_tiles * kTicketPitch, n = g.time_tiles * a.D;
+        p.tickets = static_cast<uint32_t *>(a.workspace);
+        p.words = reinterpret_cast<uint64_t *>(p.tickets + nt);
         hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)std::min(ceil_div(n, 256), (int64_t)2048)), dim3(256), 0, st,
-                           p.ticket, p.words, n);
+                           p.tickets, nt, p.words, n);
     }
     const dim3 grid((unsigned)(g.time_tiles * g.chan_tiles));
-    if (g.vec == 4) hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 4>), grid, dim3(kNT), 0, st, p);
-    else hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 1>), grid, dim3(kNT), 0, st, p);
+    if constexpr (sizeof(IO) == 2) {
+        if (g.vec == 2) {
+            hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 2>), grid, dim3(kNT), 0, st, p);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 1>), grid, dim3(kNT), 0, st, p);
     return hipGetLastError();
 }
 
@@ -534,11 +544,17 @@ int status(hipError_t e, char *err, size_t err_len) {
 
 // For the widest time axis of either layout (the addresses are not known here).
 size_t glr_workspace_bytes(const GlrArgs &a) {
-    const int64_t n = std::max(glr_plan(a, 4).time_tiles, glr_plan(a, 1).time_tiles);
-    return n > 1 ? 256 + (size_t)n * a.D * sizeof(uint64_t) : 0;
+    size_t need = 0;
+    for (int vec : {1, 2}) {
+        const GlrPlan g = glr_plan(a, vec);
+        if (g.time_tiles > 1)
+            need = std::max(need, (size_t)g.chan_tiles * kTicketPitch * sizeof(uint32_t) +
+                                      (size_t)g.time_tiles * a.D * sizeof(uint64_t));
+    }
+    return need;
 }
 bool glr_grids_fit(const GlrArgs &a) {
-    for (int vec : {1, 4}) {
+    for (int vec : {1, 2}) {
         const GlrPlan g = glr_plan(a, vec);
         if (g.time_tiles > kMaxWorkItems / kNT / g.chan_tiles || !grid_fits(g.time_tiles * g.chan_tiles, kNT))
             return false;
