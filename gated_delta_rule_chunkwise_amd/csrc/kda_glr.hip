@@ -13,10 +13,10 @@
 //     a batch of short ones fills its tiles like a long one;
 //   - each row composes its span; the rows' maps meet in LDS, the tile's map goes to
 //     the workspace;
-//   - tiles come in groups of kG.  The last tile of a group publishes, in place of
-//     its map, the state behind it (a map with A = 0), so a tile's incoming state is
-//     the composition of at most kG published maps, in a fixed order whatever the
-//     timing: the results are the same bits on every call;
+//   - tiles come in groups.  The last tile of a group publishes, in place of its
+//     map, the state behind it (a map with A = 0), so a tile's incoming state is the
+//     composition of at most a group of published maps, in a fixed order whatever
+//     the timing: the results are the same bits on every call;
 //   - with that state the rows run their spans once more, from registers, and write.
 //
 // A published map is one 64-bit word with its own validity (all ones: not there
@@ -37,8 +37,12 @@ namespace {
 
 constexpr int kW = 8;              // waves of a workgroup
 constexpr int kNT = 64 * kW;       // its threads
-constexpr int kG = 16;             // tiles of a group
+constexpr int kXcds = 8;           // chiplets, each with an L2 of its own
+constexpr int kMaxGroup = 16;      // tiles of a group at most
+constexpr int kMinSpan = 8;        // shortest span of the wide form
+constexpr int kStaged = 1024;      // borders that are kept in LDS
 constexpr int kMinLanes = 8;       // channel lanes of a row at least
+constexpr int kMaxScales = 2048;   // tokens x blocks of a tile
 constexpr int kTicketPitch = 32;   // a cache line of its own for each
 constexpr uint64_t kAbsent = ~(uint64_t)0;
 // A wait that could only be broken by a fault elsewhere still ends (after seconds),
@@ -47,21 +51,39 @@ constexpr int kMaxPolls = 1 << 24;
 
 enum Mode : int { kFwd = 0, kBwd = 1, kBwd8 = 2 };
 
-constexpr int R = 32;              // tokens of a row's span
+// Tokens of a row's span.  What a lane keeps of a token (8 bytes of x, its gates,
+// in the backward 8 more of h) times these is about 64 registers forward and 72
+// backward: two workgroups share a CU.
+template <typename IO, typename GT, int MODE, int VEC> constexpr int span_tokens() {
+    if (VEC == 1) return 32;
+    const int bytes = 8 + VEC * (int)sizeof(GT) + (MODE == 0 ? 0 : 8);
+    return bytes <= 16 ? 16 : bytes <= 24 ? (MODE == 0 ? 10 : 12) : 8;
+}
 
 // VEC consecutive values of X as loaded, and as fp32.
 template <typename X, int VEC> struct Raw;
 template <typename X> struct Raw<X, 1> { typedef X type; };
 template <> struct Raw<float, 2> { typedef float type __attribute__((ext_vector_type(2))); };
+template <> struct Raw<bf16_t, 4> { typedef bf16x4_t type; };
+// Codes stay the whole number that was loaded until they are used: bytes taken
+// apart at once would wait for the load.
+template <> struct Raw<int8_t, 4> { typedef uint32_t type; };
+template <> struct Raw<int8_t, 2> { typedef uint16_t type; };
 template <> struct Raw<bf16_t, 2> { typedef bf16x2_t type; };
-template <> struct Raw<int8_t, 2> { typedef int8_t type __attribute__((ext_vector_type(2))); };
+template <> struct Raw<float, 4> { typedef f32x4_t type; };
 
 template <int VEC, typename RAW> __device__ __forceinline__ float raw_at(const RAW &r, int e) {
-    if constexpr (VEC == 1) return (float)r;
+    if constexpr (std::is_same<RAW, uint32_t>::value || std::is_same<RAW, uint16_t>::value)
+        return (float)(int8_t)(r >> (8 * e));
+    else if constexpr (VEC == 1) return (float)r;
     else return (float)r[e];
 }
-template <typename X, int VEC> __device__ __forceinline__ typename Raw<X, VEC>::type load_raw(const X *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const typename Raw<X, VEC>::type *>(p));
+// Rows of an odd number of channels put a lane's values at any element's address:
+// the hardware loads and stores them there.
+template <typename X, int VEC, bool KEEP> __device__ __forceinline__ typename Raw<X, VEC>::type load_raw(const X *p) {
+    typedef typename Raw<X, VEC>::type at __attribute__((aligned(sizeof(X))));
+    if constexpr (KEEP) return *reinterpret_cast<const at *>(p);
+    else return __builtin_nontemporal_load(reinterpret_cast<const at *>(p));
 }
 template <typename X, int VEC> __device__ __forceinline__ void store_vec(X *p, const float (&v)[VEC]) {
     typename Raw<X, VEC>::type r;
@@ -71,7 +93,8 @@ template <typename X, int VEC> __device__ __forceinline__ void store_vec(X *p, c
 #pragma unroll
         for (int e = 0; e < VEC; ++e) r[e] = from_f32<X>(v[e]);
     }
-    __builtin_nontemporal_store(r, reinterpret_cast<typename Raw<X, VEC>::type *>(p));
+    typedef typename Raw<X, VEC>::type at __attribute__((aligned(sizeof(X))));
+    __builtin_nontemporal_store(r, reinterpret_cast<at *>(p));
 }
 template <int VEC> __device__ __forceinline__ void load_f32(const float *p, float (&v)[VEC]) {
 #pragma unroll
@@ -88,25 +111,30 @@ struct GlrParams {
     void *out, *dla;
     float *state_out;
     int64_t N, T, tokens;
-    int32_t D, chan_tiles, lane_log;   // lanes of a row: 1 << lane_log
+    int32_t D, chan_tiles, lanes;      // lanes of a row
     int64_t time_tiles;
-    uint64_t *words;                   // [time_tiles, D] published maps
+    uint64_t *words;                   // published maps: [time tile][channel tile][e][lane]
+    int32_t over;                      // h_T is written over h0
+    int32_t keep;                      // tokens share cache lines: inputs stay in the L2
+    int32_t group;                     // tiles of a group
     uint32_t *tickets;                 // one for each channel tile, kTicketPitch apart
 };
 
 // The sequences of the flat token axis.
 struct Seqs {
-    const int32_t *cu;
+    const int32_t *cu, *lds;   // the borders, or nullptr; their copy in LDS, where they are staged
+    bool staged;
     int64_t N, T;
-    __device__ __forceinline__ int64_t begin(int64_t n) const { return cu ? cu[n] : n * T; }
-    __device__ __forceinline__ int64_t end(int64_t n) const { return cu ? cu[n + 1] : (n + 1) * T; }
+    __device__ __forceinline__ int64_t border(int64_t n) const { return staged ? lds[n] : cu[n]; }
+    __device__ __forceinline__ int64_t begin(int64_t n) const { return cu ? border(n) : n * T; }
+    __device__ __forceinline__ int64_t end(int64_t n) const { return cu ? border(n + 1) : (n + 1) * T; }
     // The (non-empty) sequence of token t.
     __device__ __forceinline__ int64_t find(int64_t t) const {
         if (!cu) return t / T;
         int64_t lo = 0, hi = N - 1;   // largest n with cu[n] <= t
         while (lo < hi) {
             const int64_t mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= t) lo = mid;
+            if (border(mid) <= t) lo = mid;
             else hi = mid - 1;
         }
         return lo;
@@ -114,17 +142,37 @@ struct Seqs {
 };
 
 template <typename IO, typename GT, int MODE, int VEC> struct Row {
+    static constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     typedef typename std::conditional<MODE == kBwd8, int8_t, IO>::type HT;
     typename Raw<IO, VEC>::type x[R];
     typename Raw<GT, VEC>::type la[R];
     typename Raw<HT, VEC>::type h[R];        // backward: h of the token before
     float start[VEC];                        // forward: h0 of the last sequence that starts here
     int start_at;
+
+    template <bool KEEP> __device__ __forceinline__ void load_inputs(const GlrParams &p, int64_t t0, int nv, int c0) {
+        const IO *xp = static_cast<const IO *>(p.x) + t0 * p.D + c0;
+        const GT *gp = static_cast<const GT *>(p.la) + t0 * p.D + c0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (i < nv) {
+                la[i] = load_raw<GT, VEC, KEEP>(gp + (int64_t)i * p.D);
+                x[i] = load_raw<IO, VEC, KEEP>(xp + (int64_t)i * p.D);
+            }
+        }
+    }
+    template <bool KEEP> __device__ __forceinline__ void load_saved(const GlrParams &p, int64_t t0, int nv, int c0) {
+        const HT *hp = static_cast<const HT *>(p.h) + (t0 - 1) * p.D + c0;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < nv && t0 + i > 0) h[i] = load_raw<HT, VEC, KEEP>(hp + (int64_t)i * p.D);
+    }
 };
 
 // ---- the span of one row, all of it inside one sequence ------------------------
 template <typename IO, typename GT, int MODE, int VEC>
 __device__ __forceinline__ void compose_inside(const Row<IO, GT, MODE, VEC> &row, float (&L)[VEC], float (&B)[VEC]) {
+    constexpr int R = span_tokens<IO, GT, MODE, VEC>();
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int i = MODE == kFwd ? k : R - 1 - k;
@@ -139,7 +187,8 @@ __device__ __forceinline__ void compose_inside(const Row<IO, GT, MODE, VEC> &row
 
 template <typename IO, typename GT, int MODE, int VEC>
 __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, GT, MODE, VEC> &row, const float *hs,
-                                              int64_t t0, int c0, float (&s)[VEC]) {
+                                              int64_t t0, int c0, int skip, float (&s)[VEC]) {
+    constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     IO *out = static_cast<IO *>(p.out);
     GT *dla = static_cast<GT *>(p.dla);
 #pragma unroll
@@ -161,7 +210,13 @@ __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, 
                 d[e] = a == 0.f ? 0.f : h * s[e];
             }
         }
-        store_vec<IO, VEC>(out + at, o);
+        if (skip) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= skip) out[at + e] = from_f32<IO>(o[e]);
+        } else {
+            store_vec<IO, VEC>(out + at, o);
+        }
         if constexpr (MODE != kFwd) store_vec<GT, VEC>(dla + at, d);
     }
 }
@@ -173,6 +228,7 @@ __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, 
 template <typename IO, typename GT, int MODE, int VEC>
 __device__ __forceinline__ void compose_border(const GlrParams &p, const Seqs &q, Row<IO, GT, MODE, VEC> &row,
                                                int64_t t0, int nv, int c0, float (&L)[VEC], float (&B)[VEC]) {
+    constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     row.start_at = -1;
     if (nv <= 0) return;
     int64_t n = q.find(MODE == kFwd ? t0 : t0 + nv - 1), b = q.begin(n), e_ = q.end(n);
@@ -214,7 +270,9 @@ __device__ __forceinline__ void compose_border(const GlrParams &p, const Seqs &q
 
 template <typename IO, typename GT, int MODE, int VEC>
 __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q, const Row<IO, GT, MODE, VEC> &row,
-                                              const float *hs, int64_t t0, int nv, int c0, float (&s)[VEC]) {
+                                              const float *hs, int64_t t0, int nv, int c0, int skip,
+                                              float (&s)[VEC]) {
+    constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     if (nv <= 0) return;
     IO *out = static_cast<IO *>(p.out);
     GT *dla = static_cast<GT *>(p.dla);
@@ -261,12 +319,19 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
                 d[e] = a == 0.f ? 0.f : h[e] * s[e];
             }
         }
-        store_vec<IO, VEC>(out + at, o);
+        if (skip) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (e >= skip) out[at + e] = from_f32<IO>(o[e]);
+        } else {
+            store_vec<IO, VEC>(out + at, o);
+        }
         if constexpr (MODE != kFwd) store_vec<GT, VEC>(dla + at, d);
         if (MODE == kFwd ? t + 1 == e_ : t == b) {
             if (p.state_out) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) p.state_out[n * p.D + c0 + e] = s[e];
+                for (int e = 0; e < VEC; ++e)
+                    if (e >= skip) p.state_out[n * p.D + c0 + e] = s[e];
             }
             if constexpr (MODE == kFwd) {
                 if (i + 1 < nv) {
@@ -283,173 +348,213 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
     }
 }
 
-template <int MODE, int VEC> struct alignas(16) GlrShared {
-    float A[kNT * VEC], B[kNT * VEC];               // the rows' maps
-    float pA[kG][64 * VEC], pB[kG][64 * VEC];       // the published maps in front of the tile
-    float hs[MODE == kBwd8 ? kNT / kMinLanes * R : 1];   // scales of the rows' saved h
+// A map s -> a s + b of a lane's channels.
+template <int VEC> struct alignas(VEC * 8) Map {
+    float a[VEC], b[VEC];
+    __device__ __forceinline__ void then(const Map &m) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            b[e] = decayed(m.a[e], b[e]) + m.b[e];
+            a[e] *= m.a[e];
+        }
+    }
+    // then m[0], m[stride], .., n of them: loads in batches, so that their latency
+    // is paid once for each four
+    __device__ __forceinline__ void then_all(const Map *m, int stride, int n) {
+        for (int j = 0; j < n; j += 4) {
+            Map w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = m[min(j + k, n - 1) * stride];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j + k < n) then(w[k]);
+        }
+    }
+};
+
+template <int MODE, int VEC> struct alignas(32) GlrShared {
+    Map<VEC> row[kNT];                              // the rows' maps
+    Map<VEC> pre[kMaxGroup][64];                    // the maps of the group's tiles in front of this one
+    float state[64 * VEC];                          // the state behind the last group
+    float hs[MODE == kBwd8 ? kMaxScales : 1];       // scales of the tile's saved h
+    int32_t cu[kStaged];
     uint32_t tile;
 };
 
 template <typename IO, typename GT, int MODE, int VEC>
-__global__ __launch_bounds__(kNT) void glr_kernel(const GlrParams p) {
-    typedef typename Row<IO, GT, MODE, VEC>::HT HT;
+__global__ __launch_bounds__(kNT, 4) void glr_kernel(const GlrParams p) {
+    constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     __shared__ GlrShared<MODE, VEC> sm;
+    // Workgroups go to the 8 XCDs in turn: the channel tiles of a time tile follow one
+    // another on the same XCD, whose L2 joins what they have of shared lines.
     const int tid = threadIdx.x;
-    const int ct = (int)(blockIdx.x % p.chan_tiles);
-    int64_t tt = 0;                                    // in the order of the scan
-    if (p.time_tiles > 1) {
-        if (tid == 0)
-            sm.tile = __hip_atomic_fetch_add(p.tickets + ct * kTicketPitch, 1u, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        tt = sm.tile;
-    }
-    const int lanes = 1 << p.lane_log, rows = kNT >> p.lane_log;
-    const int cl = tid & (lanes - 1), v = tid >> p.lane_log;   // lane of a row, row in the order of the scan
-    const int c0 = (ct * lanes + cl) * VEC;
-    const bool chan = c0 < p.D;
-    const Seqs q = {p.cu, p.N, p.T};
+    const int ct = (int)(p.time_tiles > 1 ? blockIdx.x / kXcds % p.chan_tiles : blockIdx.x);
+    const bool staged = p.cu && p.N < kStaged;
     int64_t valid = p.tokens;                          // rows behind the last sequence are not touched
     if (p.cu) valid = min(valid, (int64_t)p.cu[p.N]);
+    if (staged)
+        for (int i = tid; i <= (int)p.N; i += kNT) sm.cu[i] = p.cu[i];
+    if (p.time_tiles > 1 && tid == 0)
+        sm.tile = __hip_atomic_fetch_add(p.tickets + ct * kTicketPitch, 1u, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    if (p.time_tiles > 1 || staged) __syncthreads();
+    const int64_t tt = p.time_tiles > 1 ? sm.tile : 0;   // in the order of the scan
+    if (tt >= p.time_tiles) return;                      // of a grid rounded up to whole XCDs
+    const int lanes = p.lanes, rows = kNT / lanes;
+    const int v = tid / lanes, cl = tid - v * lanes;     // row in the order of the scan, lane of it
+    // where VEC does not divide D, the last lane's channels overlap its neighbour's:
+    // both compute and write the same values
+    const int cv = (ct * lanes + cl) * VEC, c0 = min(cv, p.D - VEC);
+    const bool chan = cv < p.D && v < rows, last = v == rows - 1;
+    // With h_T over h0 the neighbour's h_T may be there before the last lane reads
+    // h0: what that lane has for the shared channels is not written then.
+    const int skip = MODE == kFwd && p.over ? cv - c0 : 0;
+    const Seqs q = {p.cu, sm.cu, staged, p.N, p.T};
     const int64_t span = MODE == kFwd ? tt * rows + v : (p.time_tiles - 1 - tt) * rows + (rows - 1 - v);
     const int64_t t0 = span * R;
     const int nv = chan ? (int)max((int64_t)0, min((int64_t)R, valid - t0)) : 0;
 
+    // scales of the saved h: [block of the tile][token of the tile]
+    const int b0 = ct * lanes * VEC / kAct8Block, nt = rows * R;
+    float hsv[kMaxScales / kNT];
+    if constexpr (MODE == kBwd8) {
+        const int nb = (p.D + kAct8Block - 1) / kAct8Block;
+        const int blocks = (min((ct + 1) * lanes * VEC, p.D) - 1) / kAct8Block - b0 + 1;
+        const int64_t tile0 = (p.time_tiles - 1 - tt) * nt;
+#pragma unroll
+        for (int k = 0; k < kMaxScales / kNT; ++k) {
+            const int i = tid + k * kNT, b = i / nt;
+            const int64_t t = tile0 + i - b * nt;
+            hsv[k] = b < blocks && t > 0 && t < valid ? p.hs[(t - 1) * nb + b0 + b] : 0.f;
+        }
+    }
     Row<IO, GT, MODE, VEC> row;
-    {
-        const IO *x = static_cast<const IO *>(p.x) + t0 * p.D + c0;
-        const GT *la = static_cast<const GT *>(p.la) + t0 * p.D + c0;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (i < nv) {
-                row.la[i] = load_raw<GT, VEC>(la + (int64_t)i * p.D);
-                row.x[i] = load_raw<IO, VEC>(x + (int64_t)i * p.D);
-            }
-        }
-    }
-    if (p.state_out) {   // empty sequences pass their state on
-        for (int64_t n = tt; n < p.N; n += p.time_tiles) {
-            if (v == 0 && chan && q.begin(n) == q.end(n)) {
-                const float *src = MODE == kFwd ? p.h0 : p.g_hT;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) p.state_out[n * p.D + c0 + e] = src ? src[n * p.D + c0 + e] : 0.f;
-            }
-        }
-    }
+    if (p.keep) row.template load_inputs<true>(p, t0, nv, c0);
+    else row.template load_inputs<false>(p, t0, nv, c0);
     bool inside = nv == R || !chan;
     if (nv == R) {
         const int64_t n = q.find(t0);
         inside = q.begin(n) < t0 && q.end(n) > t0 + R;
     }
     const bool plain = __all(inside) && __any(chan);
-
-    float L[VEC], A[VEC], B[VEC];
+    if (p.state_out) {   // empty sequences pass their state on
+        for (int64_t n = tt; n < p.N; n += p.time_tiles) {
+            if (v == 0 && chan && q.begin(n) == q.end(n)) {
+                const float *src = MODE == kFwd ? p.h0 : p.g_hT;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) L[e] = 0.f, B[e] = 0.f;
+                for (int e = 0; e < VEC; ++e)
+                    p.state_out[n * p.D + c0 + e] = src ? src[n * p.D + c0 + e] : 0.f;
+            }
+        }
+    }
+
+    float L[VEC];
+    Map<VEC> own;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) L[e] = 0.f, own.b[e] = 0.f;
     if (plain) {
-        if (chan) compose_inside<IO, GT, MODE, VEC>(row, L, B);
+        if (chan) compose_inside<IO, GT, MODE, VEC>(row, L, own.b);
     } else {
-        compose_border<IO, GT, MODE, VEC>(p, q, row, t0, nv, c0, L, B);
+        compose_border<IO, GT, MODE, VEC>(p, q, row, t0, nv, c0, L, own.b);
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        A[e] = __expf(L[e]);
-        sm.A[tid * VEC + e] = A[e];
-        sm.B[tid * VEC + e] = B[e];
+    for (int e = 0; e < VEC; ++e) own.a[e] = __expf(L[e]);
+    sm.row[tid] = own;
+    if constexpr (MODE == kBwd8) {
+#pragma unroll
+        for (int k = 0; k < kMaxScales / kNT; ++k) sm.hs[tid + k * kNT] = hsv[k];
     }
     if constexpr (MODE != kFwd) {
-        const HT *h = static_cast<const HT *>(p.h) + (t0 - 1) * p.D + c0;
-        const int nb = (p.D + kAct8Block - 1) / kAct8Block;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (i < nv && t0 + i > 0) {
-                row.h[i] = load_raw<HT, VEC>(h + (int64_t)i * p.D);
-            }
-        }
-        if constexpr (MODE == kBwd8) {   // a tile's channels lie in one block of 128
-            const int64_t tile0 = (p.time_tiles - 1 - tt) * rows * R;
-            for (int i = tid; i < rows * R; i += kNT) {
-                const int64_t t = tile0 + i;
-                if (t > 0 && t < valid) sm.hs[i] = p.hs[(t - 1) * nb + ct * lanes * VEC / kAct8Block];
-            }
-        }
+        if (p.keep) row.template load_saved<true>(p, t0, nv, c0);
+        else row.template load_saved<false>(p, t0, nv, c0);
     }
     __syncthreads();
 
-    float s[VEC];   // the state in front of this tile
+    Map<VEC> s;   // its b: the state in front of this row
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s[e] = 0.f;
+    for (int e = 0; e < VEC; ++e) s.a[e] = 1.f, s.b[e] = 0.f;
     if (p.time_tiles > 1) {
-        const int pos = (int)(tt % kG);
-        const int64_t first = tt - pos > 0 ? tt - pos - 1 : 0;   // the state behind the last group, or the first map
-        const int cnt = (int)(tt - first);
-        if (v == rows - 1) {
-            // the tile's map: the rows in front of this one, then this one
+        const int pos = (int)(tt % p.group);         // tiles of the group in front of this one
+        const bool anchored = tt >= p.group, closes = pos == p.group - 1;
+        // a wave's words of one e are consecutive: whole lines to and from memory
+        const int64_t pitch = (int64_t)p.chan_tiles * lanes * VEC;
+        uint64_t *const words = p.words + (int64_t)ct * lanes * VEC + cl;
+        const auto publish = [&](const Map<VEC> &m) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                float a = 1.f, b = 0.f;
-                for (int u = 0; u < rows; ++u) {
-                    const int k = (u * lanes + cl) * VEC + e;
-                    b = decayed(sm.A[k], b) + sm.B[k];
-                    a *= sm.A[k];
-                }
-                A[e] = a;
-                B[e] = b;
+                uint32_t ab = __builtin_bit_cast(uint32_t, m.a[e]);
+                if (ab == 0xffffffffu) ab = 0x7fc00000u;
+                __hip_atomic_store(words + tt * pitch + e * lanes,
+                                   (uint64_t)__builtin_bit_cast(uint32_t, m.b[e]) << 32 | ab, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
             }
-        }
-        const auto publish = [&](int e, float a, float b) {
-            uint32_t ab = __builtin_bit_cast(uint32_t, a);
-            if (ab == 0xffffffffu) ab = 0x7fc00000u;
-            __hip_atomic_store(p.words + tt * p.D + c0 + e, (uint64_t)__builtin_bit_cast(uint32_t, b) << 32 | ab,
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         };
-        if (v == rows - 1 && chan && pos != kG - 1) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) publish(e, A[e], B[e]);
-        }
-        for (int j = v; j < cnt; j += rows) {
-            const uint64_t *w = p.words + (first + j) * p.D + c0;
+        const auto await = [&](int64_t tile) {
+            const uint64_t *w = words + tile * pitch;
             uint64_t got[VEC];
-            int polls = 0;
-            bool there = !chan;
-            while (!there && polls < kMaxPolls) {
+            bool there = false;
+            for (int polls = 0; !there && polls < kMaxPolls; ++polls) {
+                if (polls) __builtin_amdgcn_s_sleep(1);
                 there = true;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    got[e] = __hip_atomic_load(w + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    got[e] = __hip_atomic_load(w + e * lanes, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) there = there && (uint32_t)got[e] != 0xffffffffu;
-                if (!there) __builtin_amdgcn_s_sleep(1);
-                ++polls;
             }
+            Map<VEC> m;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float nan = __builtin_nanf("");
-                sm.pA[j][cl * VEC + e] = there && chan ? __builtin_bit_cast(float, (uint32_t)got[e]) : nan;
-                sm.pB[j][cl * VEC + e] = there && chan ? __builtin_bit_cast(float, (uint32_t)(got[e] >> 32)) : nan;
+                m.a[e] = there ? __builtin_bit_cast(float, (uint32_t)got[e]) : __builtin_nanf("");
+                m.b[e] = there ? __builtin_bit_cast(float, (uint32_t)(got[e] >> 32)) : __builtin_nanf("");
+            }
+            return m;
+        };
+        Map<VEC> tile = s;   // the tile's map
+        if (last && chan) {
+            tile.then_all(sm.row + cl, lanes, rows);
+            if (!closes) publish(tile);
+        }
+        if (chan)
+            for (int j = v; j < pos; j += rows) sm.pre[j][cl] = await(tt - pos + j);
+        if (pos) {
+            __syncthreads();
+            if (chan) s.then_all(&sm.pre[0][cl], 64, pos);
+        }
+        // The state behind the last group comes last, and what follows from it is
+        // short: this is the chain that a long sequence waits for.
+        if (last && chan) {
+            Map<VEC> in = s;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) in.b[e] = 0.f;
+            if (anchored) in = await(tt - pos - 1);
+            if (closes) {
+                Map<VEC> out = in;
+                out.then(s);
+                out.then(tile);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) out.a[e] = 0.f;
+                publish(out);
+            }
+            if (anchored)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) sm.state[cl * VEC + e] = in.b[e];
+        }
+        if (anchored) {
+            __syncthreads();
+            if (chan) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s.b[e] += decayed(s.a[e], sm.state[cl * VEC + e]);
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            for (int j = 0; j < cnt; ++j) s[e] = decayed(sm.pA[j][cl * VEC + e], s[e]) + sm.pB[j][cl * VEC + e];
-        if (v == rows - 1 && chan && pos == kG - 1) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) publish(e, 0.f, decayed(A[e], s[e]) + B[e]);
-        }
     }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        for (int u = 0; u < v; ++u) {
-            const int k = (u * lanes + cl) * VEC + e;
-            s[e] = decayed(sm.A[k], s[e]) + sm.B[k];
-        }
-    }
-    const float *hs = sm.hs + (MODE == kBwd8 ? (rows - 1 - v) * R : 0);
+    if (chan) s.then_all(sm.row + cl, lanes, v);
+    const float *hs = sm.hs;
+    if constexpr (MODE == kBwd8) hs += (c0 / kAct8Block - b0) * nt + (rows - 1 - v) * R;
     if (plain) {
-        if (chan) finish_inside<IO, GT, MODE, VEC>(p, row, hs, t0, c0, s);
+        if (chan) finish_inside<IO, GT, MODE, VEC>(p, row, hs, t0, c0, skip, s.b);
     } else {
-        finish_border<IO, GT, MODE, VEC>(p, q, row, hs, t0, nv, c0, s);
+        finish_border<IO, GT, MODE, VEC>(p, q, row, hs, t0, nv, c0, skip, s.b);
     }
 }
 
@@ -474,52 +579,71 @@ __global__ __launch_bounds__(kThreads) void glr_step_kernel(const IO *__restrict
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct GlrPlan {
-    int vec, lane_log;
+    int vec, lanes;
     int64_t chan_tiles, time_tiles;
 };
-// Two channels a lane in bf16 where the addresses allow it, one otherwise: a wave's
-// load is 256 bytes of a token (128 in the odd bf16 case).  A row of lanes covers
-// the channels up to a wave's width; with fewer channels a wave takes several rows.
-GlrPlan glr_plan(const GlrArgs &a, int vec) {
+// Eight bytes of a token a lane (four channels in bf16, two in fp32), or one
+// channel.  The channels are split evenly over rows of at most 64 lanes; rows may
+// lie across waves.
+GlrPlan glr_plan(const GlrArgs &a, int vec, int span) {
     GlrPlan g = {};
     g.vec = vec;
     const int64_t need = ceil_div(a.D, vec);
-    g.lane_log = 3;
-    while (g.lane_log < 6 && (1 << g.lane_log) < need) ++g.lane_log;
-    g.chan_tiles = ceil_div(need, (int64_t)1 << g.lane_log);
-    const int64_t tile = (int64_t)(kNT >> g.lane_log) * R;
+    g.chan_tiles = ceil_div(need, 64);
+    g.lanes = (int)std::max(ceil_div(need, g.chan_tiles), (int64_t)kMinLanes);
+    const int64_t tile = (int64_t)(kNT / g.lanes) * span;
     g.time_tiles = a.tokens > tile ? ceil_div(a.tokens, tile) : 1;
     return g;
 }
-static_assert(kMinLanes == 8, "the plan's smallest row");
+int64_t glr_words(const GlrPlan &g) { return g.time_tiles * g.chan_tiles * g.lanes * g.vec; }
+int64_t glr_grid(const GlrPlan &g) {
+    return g.time_tiles > 1 ? ceil_div(g.time_tiles, kXcds) * kXcds * g.chan_tiles : g.chan_tiles;
+}
+// Tiles of a group.  A tile reads up to as many published maps, and a sequence's
+// state passes through one group after the other.  With many channel tiles few time
+// tiles run at once and the reads count; with few of them the chain does.
+int32_t glr_group(const GlrPlan &g) { return g.chan_tiles >= 16 ? 8 : kMaxGroup; }
+// The scales of a tile: a row of at least kMinLanes lanes has its channels in one
+// block of 128, of more than 32 in at most three.
+static_assert(kNT / kMinLanes * 32 <= kMaxScales && kNT / 33 * 32 * 3 <= kMaxScales, "scales of a tile");
 
-bool glr_aligned(const GlrArgs &a) {
-    const auto ok = [](const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
-    const uintptr_t gt = a.gate_bf16 ? 4 : 8;
-    return a.D % 2 == 0 && ok(a.x, 4) && ok(a.out, 4) && ok(a.log_alpha, gt) && ok(a.dlog_alpha, gt) &&
-           ok(a.h_in, a.h_scales ? 2 : 4);
+// One channel a lane is for what the wide form cannot do: fewer channels than it
+// takes, and an overlap of lanes that lies across a border of 128 saved codes (in
+// either backward, so that both take the same sums).
+int glr_vec(const GlrArgs &a) {
+    const int vec = a.io_bf16 ? 4 : 2;
+    if (a.D % vec == 0) return vec;
+    return a.D < vec || (a.backward && a.D % kAct8Block < vec) ? 1 : vec;
+}
+// The tilings that a call of these sizes may take: the longest time axis of each.
+template <typename F> void glr_each_plan(const GlrArgs &a, F f) {
+    f(glr_plan(a, 1, 32));
+    f(glr_plan(a, a.io_bf16 ? 4 : 2, kMinSpan));
 }
 
 template <typename IO, typename GT, int MODE> hipError_t launch_m(const GlrArgs &a, hipStream_t st) {
-    const GlrPlan g = glr_plan(a, a.io_bf16 && glr_aligned(a) ? 2 : 1);
+    constexpr int kWide = 8 / sizeof(IO), kWideSpan = span_tokens<IO, GT, MODE, kWide>();
+    static_assert(kWideSpan >= kMinSpan && span_tokens<IO, GT, MODE, 1>() == 32, "the workspace's plans");
+    const int vec = glr_vec(a);
+    const GlrPlan g = glr_plan(a, vec, vec > 1 ? kWideSpan : 32);
+    // a line that two channel tiles read is read from memory once if it is kept
+    // (387 fp32 channels: 192 against 203 us for 139,000 tokens); whole lines are read
+    // once and stream past the L2 (65536 x 4096 bf16: 318 against 332 us)
+    const bool keep = a.D * sizeof(IO) % 128 != 0 || reinterpret_cast<uintptr_t>(a.x) % 128 != 0;
     GlrParams p = {a.x, a.log_alpha, a.h_in, a.h_scales, a.h0, a.d_hT, a.cu_seqlens, a.out, a.dlog_alpha, a.state_out,
-                   a.num_seqs, a.seq_len, a.tokens, a.D, (int32_t)g.chan_tiles, g.lane_log, g.time_tiles, nullptr,
-                   nullptr};
+                   a.num_seqs, a.seq_len, a.tokens, a.D, (int32_t)g.chan_tiles, g.lanes, g.time_tiles, nullptr,
+                   !a.backward && a.state_out && a.state_out == a.h0, keep,
+                   glr_group(g), nullptr};
     if (g.time_tiles > 1) {
-        const int64_t nt = g.chan_tiles * kTicketPitch, n = g.time_tiles * a.D;
+        const int64_t nt = g.chan_tiles * kTicketPitch, n = glr_words(g);
         p.tickets = static_cast<uint32_t *>(a.workspace);
         p.words = reinterpret_cast<uint64_t *>(p.tickets + nt);
         hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)std::min(ceil_div(n, 256), (int64_t)2048)), dim3(256), 0, st,
                            p.tickets, nt, p.words, n);
     }
-    const dim3 grid((unsigned)(g.time_tiles * g.chan_tiles));
-    if constexpr (sizeof(IO) == 2) {
-        if (g.vec == 2) {
-            hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 2>), grid, dim3(kNT), 0, st, p);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 1>), grid, dim3(kNT), 0, st, p);
+    const dim3 grid((unsigned)glr_grid(g));
+    if (g.vec > 1) hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, kWide>), grid, dim3(kNT), 0, st, p);
+    else hipLaunchKernelGGL((glr_kernel<IO, GT, MODE, 1>), grid, dim3(kNT), 0, st, p);
     return hipGetLastError();
 }
 
@@ -542,24 +666,21 @@ int status(hipError_t e, char *err, size_t err_len) {
 
 }  // namespace
 
-// For the widest time axis of either layout (the addresses are not known here).
 size_t glr_workspace_bytes(const GlrArgs &a) {
     size_t need = 0;
-    for (int vec : {1, 2}) {
-        const GlrPlan g = glr_plan(a, vec);
+    glr_each_plan(a, [&](const GlrPlan &g) {
         if (g.time_tiles > 1)
             need = std::max(need, (size_t)g.chan_tiles * kTicketPitch * sizeof(uint32_t) +
-                                      (size_t)g.time_tiles * a.D * sizeof(uint64_t));
-    }
+                                      (size_t)glr_words(g) * sizeof(uint64_t));
+    });
     return need;
 }
 bool glr_grids_fit(const GlrArgs &a) {
-    for (int vec : {1, 2}) {
-        const GlrPlan g = glr_plan(a, vec);
-        if (g.time_tiles > kMaxWorkItems / kNT / g.chan_tiles || !grid_fits(g.time_tiles * g.chan_tiles, kNT))
-            return false;
-    }
-    return true;
+    bool fit = true;
+    glr_each_plan(a, [&](const GlrPlan &g) {
+        fit = fit && g.time_tiles <= kMaxWorkItems / kNT / g.chan_tiles && grid_fits(glr_grid(g), kNT);
+    });
+    return fit;
 }
 bool glr_step_grids_fit(const GlrStepArgs &a) { return grid_fits(ceil_div(a.n, kThreads), kThreads); }
 
