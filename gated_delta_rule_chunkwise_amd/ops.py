@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import sys
 
 ACT8_BLOCK = 128   # values that share a scale
 
@@ -41,9 +42,19 @@ def declare(lib):
         fn.restype, fn.argtypes = res, args
 
 
-def _pkg():
-    import gated_delta_rule_chunkwise_amd as kda
-    return kda
+kda = sys.modules[__package__]   # the package: its library handle, type codes and errors
+
+
+class _LazyTorch:
+    """torch, imported at its first use; from then on the module itself."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _LazyTorch()
 
 
 def _p(t):
@@ -55,17 +66,17 @@ _SAME = contextlib.nullcontext()
 
 def _on(dev):
     """The tensors' device as the current one: kernels are launched on it."""
-    import torch
     return _SAME if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _stream(dev):
-    import torch
-    return torch.cuda.current_stream(dev).cuda_stream
+    """The current stream's handle.  A call of a few microseconds is half spent on
+    making torch's stream object, so the handle is asked for directly."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _need(name, t, dev, shape=None, dtype=None):
-    if not t.is_cuda or t.device != dev:
+    if t.device != dev:
         raise ValueError("%s must be on %s" % (name, dev))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -83,7 +94,6 @@ def _device_of(name, t):
 
 def _check(rc, name):
     if rc != 0:
-        kda = _pkg()
         raise kda.KDAError(rc, name, kda.kda_last_hip_error())
 
 
@@ -93,12 +103,11 @@ def _blocks(cols):
 
 # ------------------------------------------------- gated linear recurrence
 def kda_glr_workspace_size(B, T, D, num_seqs=0, io_dtype=1) -> int:
-    return int(_pkg().load_library().kda_glr_workspace_size(B, T, D, num_seqs, io_dtype))
+    return int(kda.load_library().kda_glr_workspace_size(B, T, D, num_seqs, io_dtype))
 
 
 def _glr_sizes(like, cu_seqlens, dev):
     """(B, T, D, N, packed) of a [B, T, D] or, for one sequence or a packed batch, [T, D] tensor."""
-    import torch
     if like.dim() not in (2, 3):
         raise ValueError("expected [B, T, D] or [T, D], not %s" % (tuple(like.shape),))
     B, T, D = (1,) * (3 - like.dim()) + tuple(like.shape)
@@ -109,7 +118,6 @@ def _glr_sizes(like, cu_seqlens, dev):
 
 
 def _glr_workspace(lib, B, T, D, nseq, io, workspace, dev):
-    import torch
     if workspace is None:
         need = lib.kda_glr_workspace_size(B, T, D, nseq, io)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -126,8 +134,6 @@ def kda_glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_T=None, out
     cu_seqlens: int32 [N+1] on the device (B must be 1) or None.  log_alpha = -inf
     is a reset.  Returns (h, h_T), h_T [N, D] fp32 or None when
     output_final_state is False."""
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("x", x)
     _need("x", x, dev)
@@ -154,8 +160,6 @@ def kda_glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_T=None, out
 
 
 def _glr_bwd(name, log_alpha, h, scales, grad_h, h0, grad_hT, cu_seqlens, want_grad_h0, workspace):
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("grad_h", grad_h)
     f32 = torch.float32
@@ -197,8 +201,6 @@ def kda_glr_bwd_act8(log_alpha, h_codes, h_scales, grad_h, h0=None, grad_hT=None
 
 def kda_glr_step(x, log_alpha, S, h=None):
     """One token of kda_glr_fwd: x, log_alpha [B, D]; S [B, D] fp32, updated in place.  Returns h."""
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("x", x)
     if x.dim() != 2:
@@ -229,8 +231,6 @@ def _rows_cols(name, t):
 def kda_act8_pack(x, *, codes=None, scales=None):
     """x [..., d] in 8 bits: (codes int8 [..., d], scales fp32 [..., ceil(d / 128)]),
     one scale for each 128 consecutive values of the last axis."""
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("x", x)
     _need("x", x, dev)
@@ -253,8 +253,6 @@ def kda_act8_pack(x, *, codes=None, scales=None):
 def kda_act8_unpack(codes, scales, dtype=None, *, out=None):
     """The values that codes and scales (kda_act8_pack) stand for, in dtype
     (bfloat16 unless given)."""
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("codes", codes)
     _need("codes", codes, dev, dtype=torch.int8)
@@ -271,12 +269,10 @@ def kda_act8_unpack(codes, scales, dtype=None, *, out=None):
 
 
 def kda_chunk_bwd_act8_workspace_size(B, T, H, d_k, d_v, num_seqs=0, io_dtype=1) -> int:
-    return int(_pkg().load_library().kda_chunk_bwd_act8_workspace_size(B, T, H, d_k, d_v, num_seqs, io_dtype))
+    return int(kda.load_library().kda_chunk_bwd_act8_workspace_size(B, T, H, d_k, d_v, num_seqs, io_dtype))
 
 
 def _chunk_bwd_act8(name, q8, k8, v8, log_alpha, beta, grad_o, h0, grad_hT, cu_seqlens, want_grad_h0, workspace):
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     gdn = name == "kda_gdn_chunk_bwd_act8"
     dev = _device_of("grad_o", grad_o)
@@ -339,8 +335,6 @@ def kda_gdn_chunk_bwd_act8(q8, k8, v8, log_alpha, beta, grad_o, h0=None, grad_hT
 
 # ------------------------------------------------------------------- RMS norm
 def _norm_fwd(name, x, weight, residual, eps, y, codes, scales, r, want_rstd):
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("x", x)
     f32 = torch.float32
@@ -400,12 +394,10 @@ def kda_rmsnorm_fwd_act8(x, weight=None, residual=None, eps=1e-6, *, codes=None,
 
 
 def kda_rmsnorm_bwd_workspace_size(rows, cols) -> int:
-    return int(_pkg().load_library().kda_rmsnorm_bwd_workspace_size(rows, cols))
+    return int(kda.load_library().kda_rmsnorm_bwd_workspace_size(rows, cols))
 
 
 def _norm_bwd(name, r, scales, weight, rstd, grad_y, grad_r, want_grad_weight, grad_x, workspace):
-    import torch
-    kda = _pkg()
     lib = kda.load_library()
     dev = _device_of("grad_y", grad_y)
     f32 = torch.float32
@@ -465,8 +457,6 @@ _FUNCTIONS = {}
 def _function(name):
     """The autograd functions, made on first use (torch is imported lazily)."""
     if not _FUNCTIONS:
-        import torch
-
         class _GLR(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, log_alpha, h0, cu_seqlens, act8):
