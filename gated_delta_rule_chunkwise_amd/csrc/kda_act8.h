@@ -1,5 +1,5 @@
 // The 8-bit form of a block of values, shared by the kernels that write or read
-// it (gfx950 only): scale = max|x| / 127 in fp32, code = x / scale to nearest.
+// it (gfx950 only): scale = max|x| (1 / 127) in fp32, code = x / scale to nearest.
 #pragma once
 #include <type_traits>
 
@@ -9,7 +9,9 @@ namespace kda {
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr float kAct8Tiny = 1.17549435e-38f;    // 2^-126: 1 / scale stays finite
-constexpr float kAct8Huge = 2.67938851e36f;     // largest scale with 127 * scale finite
+// 1 / 127 to nearest is 127's exact inverse to 4e-9: 127 scales are max|x| to half a
+// step of fp32, and finite for every finite max|x|.
+constexpr float kAct8Step = 1.f / 127.f;
 
 // The largest magnitude is taken over the bit patterns without their sign: as
 // whole numbers they order finite values, then infinity, then NaN, so a value
@@ -18,7 +20,7 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cas
 
 __device__ __forceinline__ float act8_scale(uint32_t amax_bits) {
     if (amax_bits >= kInfBits) return __builtin_nanf("");
-    return fminf(fmaxf(__builtin_bit_cast(float, amax_bits) / 127.f, kAct8Tiny), kAct8Huge);
+    return fmaxf(__builtin_bit_cast(float, amax_bits) * kAct8Step, kAct8Tiny);
 }
 
 // x / s rounded to nearest, ties of the exact quotient to even.  The product with

@@ -558,9 +558,10 @@ kda_status_t kda_glr_step(const void *x, const void *log_alpha, float *S, void *
  * block of 128 consecutive values of a row (the last block of a row may be
  * shorter) is held as whole numbers -127..127 and one fp32 scale:
  *
- *     scale = max(max|x| / 127, 2^-126),   code = x / scale rounded to nearest
+ *     scale = max(max|x| * (1 / 127), 2^-126),   code = x / scale rounded to nearest
  *
- * (ties of the exact quotient to the even code), so that code * scale is within
+ * (the product in fp32, with 1 / 127 rounded to fp32; ties of the exact quotient go
+ * to the even code), so that code * scale is within
  * scale / 2 of x.  A block that holds an infinity or a NaN gets a NaN scale and
  * codes 0: it reads back as NaN throughout.
  *

@@ -88,7 +88,7 @@ def pack(v):
     wide[:, :cols] = v.double()
     wide = wide.reshape(rows, -1, BLOCK)
     amax = wide.abs().amax(-1)          # NaN stays NaN
-    scale = (amax / 127).float().double().clamp(2.0 ** -126, 2.67938851e36)
+    scale = (amax.float() * torch.tensor(127.0).reciprocal()).double().clamp_min(2.0 ** -126)
     bad = ~torch.isfinite(amax)
     q = torch.round(wide / scale[..., None])
     q = torch.where(bad[..., None], 0.0, q)

@@ -349,7 +349,7 @@ def test_act8_random_quotients_near_ties():
     """fp32 rows whose values sit within a few steps of the middles between codes."""
     g = gen(17)
     amax = torch.rand(2000, 1, generator=g) * 10 + 0.1
-    s = (amax / 127).float()
+    s = amax * torch.tensor(127.0).reciprocal()
     k = torch.randint(-126, 126, (2000, 127), generator=g).float() + 0.5
     x = (k.double() * s.double()).float()
     bits = x.view(torch.int32) + torch.randint(-2, 3, x.shape, generator=g).int()
