@@ -17,6 +17,10 @@ bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 bool req(const void *p, uintptr_t a) { return p && aligned_to(p, a); }
 bool opt(const void *p, uintptr_t a) { return aligned_to(p, a); }
 
+// Row lengths above this are refused: kernels hold a position in a row, and a few
+// lanes' width behind its end, in 32 bits.
+constexpr int32_t kMaxRow = 1 << 30;
+
 // a * b stays well inside int64 for device indexing.
 bool product_fits(int64_t a, int64_t b) {
     const int64_t lim = (int64_t)1 << 50;
@@ -59,6 +63,7 @@ kda_status_t glr_impl(bool backward, const void *x, const void *log_alpha, const
         return KDA_ERR_INVALID_ARGUMENT;
     }
     if (!glr_sizes_ok(B, T, D, cu_seqlens ? num_seqs : B)) return KDA_ERR_INVALID_ARGUMENT;
+    if (D > kMaxRow) return KDA_ERR_UNSUPPORTED;
     const bool have_tokens = T > 0;
     const uintptr_t ios = dsize(io_dtype), gs = dsize(gate_dtype);
     if (have_tokens) {
@@ -88,6 +93,7 @@ kda_status_t act8_impl(bool pack, const void *x, void *out, const int8_t *codes,
                        int32_t cols, int32_t io_dtype, void *stream) {
     if (!valid_dtype(io_dtype)) return KDA_ERR_UNSUPPORTED;
     if (rows < 0 || cols <= 0 || !product_fits(rows, cols)) return KDA_ERR_INVALID_ARGUMENT;
+    if (cols > kMaxRow) return KDA_ERR_UNSUPPORTED;
     if (rows == 0) return KDA_OK;
     if (!req(pack ? x : out, dsize(io_dtype)) || !codes || !req(scales, 4)) return KDA_ERR_INVALID_ARGUMENT;
     kda::Act8Args a = {};
@@ -105,6 +111,7 @@ kda_status_t norm_fwd_impl(const void *x, const void *residual, const void *weig
                            int32_t io_dtype, int32_t w_dtype, void *stream) {
     if (!valid_dtype(io_dtype) || !valid_dtype(w_dtype)) return KDA_ERR_UNSUPPORTED;
     if (rows < 0 || cols <= 0 || !product_fits(rows, cols)) return KDA_ERR_INVALID_ARGUMENT;
+    if (cols > kMaxRow) return KDA_ERR_UNSUPPORTED;
     if (!isfinite(eps) || eps <= 0.f) return KDA_ERR_INVALID_ARGUMENT;
     const uintptr_t ios = dsize(io_dtype);
     if (!opt(weight, dsize(w_dtype)) || !opt(rstd, 4)) return KDA_ERR_INVALID_ARGUMENT;
@@ -129,6 +136,7 @@ kda_status_t norm_bwd_impl(const void *r, const int8_t *codes, const float *scal
                            size_t workspace_bytes, void *stream) {
     if (!valid_dtype(io_dtype) || !valid_dtype(w_dtype)) return KDA_ERR_UNSUPPORTED;
     if (rows < 0 || cols <= 0 || !product_fits(rows, cols)) return KDA_ERR_INVALID_ARGUMENT;
+    if (cols > kMaxRow) return KDA_ERR_UNSUPPORTED;
     const uintptr_t ios = dsize(io_dtype), ws = dsize(w_dtype);
     if (!opt(weight, ws) || !opt(grad_w, ws)) return KDA_ERR_INVALID_ARGUMENT;
     if (rows > 0) {
@@ -222,7 +230,7 @@ extern "C" {
 
 size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs, int32_t io_dtype) {
     if (!valid_dtype(io_dtype) || num_seqs < 0 || (num_seqs > 0 && B != 1)) return 0;
-    if (!glr_sizes_ok(B, T, D, num_seqs > 0 ? num_seqs : B)) return 0;
+    if (!glr_sizes_ok(B, T, D, num_seqs > 0 ? num_seqs : B) || D > kMaxRow) return 0;
     return kda::glr_workspace_bytes(glr_sizes(B, T, D, num_seqs, num_seqs > 0, io_dtype));
 }
 
@@ -324,7 +332,7 @@ kda_status_t kda_rmsnorm_fwd_act8(const void *x, const void *residual, const voi
 }
 
 size_t kda_rmsnorm_bwd_workspace_size(int64_t rows, int32_t cols) {
-    if (rows < 0 || cols <= 0 || !product_fits(rows, cols)) return 0;
+    if (rows < 0 || cols <= 0 || cols > kMaxRow || !product_fits(rows, cols)) return 0;
     return kda::norm_bwd_workspace_bytes(rows, cols);
 }
 

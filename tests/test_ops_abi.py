@@ -72,6 +72,18 @@ def test_glr_bwd_refusals(kda, kw, code):
     assert glr_bwd8(lib, **kw) == code
 
 
+def test_rows_beyond_32_bit_positions_are_refused(kda):
+    lib = kda.load_library()
+    big = (1 << 30) + 1
+    assert glr_fwd(lib, T=1, D=big) == glr_bwd(lib, T=1, D=big) == glr_bwd8(lib, T=1, D=big) == UNSUPPORTED
+    assert kda.kda_glr_workspace_size(1, 5000, big) == 0
+    assert lib.kda_act8_pack(P, P, P, 1, big, 1, None) == UNSUPPORTED
+    assert lib.kda_act8_unpack(P, P, P, 1, big, 1, None) == UNSUPPORTED
+    assert lib.kda_rmsnorm_fwd(P, None, None, P, None, None, 1, big, 1e-6, 1, 1, None) == UNSUPPORTED
+    assert lib.kda_rmsnorm_bwd(P, None, P, P, None, P, None, 1, big, 1, 1, None, 0, None) == UNSUPPORTED
+    assert kda.kda_rmsnorm_bwd_workspace_size(1, big) == 0
+
+
 def test_glr_bwd_saved_h(kda):
     lib = kda.load_library()
     assert glr_bwd(lib, h=None) == INVALID
@@ -97,7 +109,7 @@ def test_glr_workspace(kda):
 @pytest.mark.parametrize("kw,code", [
     (dict(io=9), UNSUPPORTED), (dict(gt=9), UNSUPPORTED), (dict(B=0), INVALID), (dict(D=-1), INVALID),
     (dict(x=None), INVALID), (dict(la=None), INVALID), (dict(S=None), INVALID), (dict(h=None), INVALID),
-    (dict(S=P + 2), INVALID), (dict(la=P + 2, gt=0), INVALID), (dict(B=1 << 30, D=1 << 10), UNSUPPORTED)])
+    (dict(S=P + 2), INVALID), (dict(la=P + 2, gt=0), INVALID), (dict(B=1 << 30, D=1 << 12), UNSUPPORTED)])
 def test_glr_step_refusals(kda, kw, code):
     a = dict(x=P, la=P, S=P, h=P, B=4, D=64, io=1, gt=1)
     a.update(kw)

@@ -214,6 +214,54 @@ def test_glr_in_place_state_over_long_sequences():
     assert torch.equal(got[0], want[0]) and torch.equal(s, want[1])
 
 
+@pytest.mark.parametrize("D", [131, 50, 261, 5])
+@pytest.mark.parametrize("io", [BF, F32])
+def test_glr_in_place_state_of_an_odd_number_of_channels(D, io):
+    """The last lanes' channels overlap there; sequences of one and two tokens, and
+    some that end in another tile, have their h0 overwritten by their h_T."""
+    lengths = [3000, 1, 0, 2, 700, 2, 1, 1, 0, 300]
+    x, la, h0, _, _ = glr_inputs(lengths, D, io, io, 37, "uniform")
+    cu = cu_of(lengths)
+    want = kda.kda_glr_fwd(x.to(DEV), la.to(DEV), h0=h0.to(DEV), cu_seqlens=cu)
+    for _ in range(3):
+        s = h0.to(DEV)
+        got = kda.kda_glr_fwd(x.to(DEV), la.to(DEV), h0=s, cu_seqlens=cu, h_T=s)
+        assert torch.equal(got[0], want[0]) and torch.equal(s, want[1])
+
+
+@pytest.mark.parametrize("N,D,most", [(3000, 40, 5), (1500, 132, 9)])
+def test_glr_more_sequences_than_are_staged(N, D, most):
+    lengths = torch.randint(0, most + 1, (N,), generator=gen(N)).tolist()
+    x, la, h0, gh, ghT = glr_inputs(lengths, D, BF, BF, 61, "softplus")
+    cu, g = cu_of(lengths), lambda t: t.to(DEV)  # noqa: E731
+    want = ref.glr_fwd(x, la, h0, lengths)
+    h, hT = kda.kda_glr_fwd(g(x), g(la), h0=g(h0), cu_seqlens=cu)
+    ref.assert_within(h, want[0], want[2], "h")
+    ref.assert_within(hT, want[1], want[3], "h_T")
+    wb = ref.glr_bwd(la, h.cpu(), gh, h0, ghT, lengths)
+    got = kda.kda_glr_bwd(g(la), h, g(gh), h0=g(h0), grad_hT=g(ghT), cu_seqlens=cu)
+    for a, w, e, name in zip(got, wb[:3], wb[3:], ("dx", "dla", "dh0")):
+        ref.assert_within(a, w, e, name)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_glr_gates_of_the_types_lowest_value(io):
+    """finfo.min is what masks are filled with: a reset, like -inf, however many follow."""
+    T, D = 700, 36
+    x, la, h0, gh, _ = glr_inputs([T], D, io, io, 15, "softplus")
+    low, inf = la.clone(), la.clone()
+    rows = [0, 5, 6, 7, 300, 301, 699]
+    low[rows], inf[rows] = torch.finfo(io).min, float("-inf")
+    a = kda.kda_glr_fwd(x.to(DEV), low.to(DEV), h0=h0.to(DEV))
+    b = kda.kda_glr_fwd(x.to(DEV), inf.to(DEV), h0=h0.to(DEV))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga = kda.kda_glr_bwd(low.to(DEV), a[0], gh.to(DEV), h0=h0.to(DEV))
+    gb = kda.kda_glr_bwd(inf.to(DEV), a[0], gh.to(DEV), h0=h0.to(DEV))
+    assert all(torch.equal(u, v) for u, v in zip(ga, gb)) and not torch.isnan(ga[1]).any()
+    want = ref.glr_fwd(x, inf, h0, [T])
+    ref.assert_within(a[0], want[0], want[2], "h")
+
+
 def test_glr_split_and_step_continue_a_sequence():
     T, D = 2400, 192
     x, la, h0, _, _ = glr_inputs([T], D, F32, F32, 13, "uniform")
