@@ -7,10 +7,10 @@
 // of it is known:
 //
 //   - the tokens of the whole batch are one flat axis, cut into time tiles; a tile
-//     of a channel block is one workgroup, a span of kR tokens of it one "row" of
-//     lanes (a wave, or a part of one where D is small).  A sequence's first token
-//     is a map with A = 0 (B takes h0), so sequences need no tiles of their own and
-//     a batch of short ones fills its tiles like a long one;
+//     of a channel block is one workgroup, a span of some tokens of it one "row" of
+//     up to 64 lanes.  A sequence's first token is a map with A = 0 (B takes h0), so
+//     sequences need no tiles of their own and a batch of short ones fills its tiles
+//     like a long one;
 //   - each row composes its span; the rows' maps meet in LDS, the tile's map goes to
 //     the workspace;
 //   - tiles come in groups.  The last tile of a group publishes, in place of its
@@ -21,8 +21,18 @@
 //
 // A published map is one 64-bit word with its own validity (all ones: not there
 // yet), read and written by relaxed agent-scope atomics: no fence, no flag.  Tiles
-// are handed out by a ticket in order of time, so a tile only ever waits for tiles
-// that are already running: the wait ends.
+// are handed out by a ticket in order of time, one for each channel tile, so a tile
+// only ever waits for tiles that are already running: the wait ends.
+//
+// Measured (copies on this card: 6.2 TB/s): bf16 forward of 65536 x 4096 in 306 us
+// (5.3 TB/s), backward of 65536 x 2048 in 242 us (5.5 TB/s), from 8-bit h over a
+// packed batch of 139,000 tokens x 2048 in 541 us (4.8 TB/s); without the waits for
+// other tiles the first is 8% shorter, the rest of the way is the pieces of 512 bytes
+// of a token that a wave takes.  Smaller tiles (64 tokens) and one workgroup a CU
+// (256 tokens) took 20% and 10% longer.  Rows of an odd number of channels share
+// lines at both ends of each piece: 387 fp32 channels run at 3.4 TB/s, 384 at 4.2.
+// With few channels the chain of states counts: 139,000 tokens x 256 in 99 us, 68
+// groups in turn.
 #include <stdio.h>
 
 #include <algorithm>

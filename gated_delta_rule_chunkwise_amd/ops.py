@@ -451,6 +451,9 @@ def kda_rmsnorm_bwd_act8(r_codes, r_scales, weight, rstd, grad_y, grad_r=None, *
 
 
 # ------------------------------------------------------------------- autograd
+# To capture a training step into a graph, capture the kda_* calls: torch's own
+# bookkeeping of leaf gradients belongs to the stream on which an eager graph of the
+# same leaves was built, and its backward may not run under another stream's capture.
 _FUNCTIONS = {}
 
 

@@ -502,7 +502,9 @@ size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
  * Numerics: states and every product are fp32; h is rounded to io_dtype with
  * round-to-nearest-even.  Deterministic: the same inputs give bitwise identical
  * outputs.  The products of decays over a span of tokens are formed in fp32; a
- * span whose product underflows counts as a reset.
+ * span whose product underflows counts as a reset.  alpha is rounded to fp32: under
+ * a gate that stays within 1e-4 of 1 the state's relative error grows to about
+ * 6e-8 / (1 - alpha).  Tokens behind cu_seqlens[N] are neither read nor written.
  */
 kda_status_t kda_glr_fwd(const void *x, const void *log_alpha, const float *h0, const int32_t *cu_seqlens,
                          int32_t num_seqs, void *h, float *h_T, int32_t B, int32_t T, int32_t D, int32_t io_dtype,
@@ -561,9 +563,9 @@ kda_status_t kda_glr_step(const void *x, const void *log_alpha, float *S, void *
  *     scale = max(max|x| * (1 / 127), 2^-126),   code = x / scale rounded to nearest
  *
  * (the product in fp32, with 1 / 127 rounded to fp32; ties of the exact quotient go
- * to the even code), so that code * scale is within
- * scale / 2 of x.  A block that holds an infinity or a NaN gets a NaN scale and
- * codes 0: it reads back as NaN throughout.
+ * to the even code), so that code * scale is within scale / 2 of x.  A block that
+ * holds an infinity or a NaN gets a NaN scale and codes 0: it reads back as NaN
+ * throughout.
  *
  *   x       [rows, cols]  io_dtype
  *   codes   [rows, cols]  int8 (out)
