@@ -4,7 +4,6 @@ package's ``__init__``.  Every function runs asynchronously on the current strea
 of its tensors' device."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import sys
 
@@ -61,21 +60,34 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-_SAME = contextlib.nullcontext()
+def _launch(dev, name, *args):
+    """The library's call `name` on the current stream of dev, which is made the
+    current device for it.  The device's index and the stream's handle are asked for
+    directly: torch's wrappers around them take 2 us of a call of 6."""
+    fn, index = getattr(kda.load_library(), name), dev.index
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != 0:
+        raise kda.KDAError(rc, name, kda.kda_last_hip_error())
 
 
-def _on(dev):
-    """The tensors' device as the current one: kernels are launched on it."""
-    return _SAME if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _code(t):
+    """The library's type code of a tensor (any other type is refused)."""
+    d = t.dtype
+    return 1 if d == torch.bfloat16 else 0 if d == torch.float32 else kda._dtype_code(t)
 
 
-def _stream(dev):
-    """The current stream's handle.  A call of a few microseconds is half spent on
-    making torch's stream object, so the handle is asked for directly."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+def _fits(t, dev, shape, dtype):
+    """What _need asks of a tensor, all at once: the way of calls that are right."""
+    return t.device == dev and t.shape == shape and t.dtype == dtype and t.is_contiguous()
 
 
 def _need(name, t, dev, shape=None, dtype=None):
+    if shape is not None and dtype is not None and _fits(t, dev, shape, dtype):
+        return
     if t.device != dev:
         raise ValueError("%s must be on %s" % (name, dev))
     if not t.is_contiguous():
@@ -90,11 +102,6 @@ def _device_of(name, t):
     if not t.is_cuda:
         raise ValueError("%s must be on a GPU, not on %s" % (name, t.device))
     return t.device
-
-
-def _check(rc, name):
-    if rc != 0:
-        raise kda.KDAError(rc, name, kda.kda_last_hip_error())
 
 
 def _blocks(cols):
@@ -117,9 +124,9 @@ def _glr_sizes(like, cu_seqlens, dev):
     return B, T, D, cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
 
 
-def _glr_workspace(lib, B, T, D, nseq, io, workspace, dev):
+def _glr_workspace(B, T, D, nseq, io, workspace, dev):
     if workspace is None:
-        need = lib.kda_glr_workspace_size(B, T, D, nseq, io)
+        need = kda.load_library().kda_glr_workspace_size(B, T, D, nseq, io)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     else:
         _need("workspace", workspace, dev)
@@ -134,15 +141,15 @@ def kda_glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_T=None, out
     cu_seqlens: int32 [N+1] on the device (B must be 1) or None.  log_alpha = -inf
     is a reset.  Returns (h, h_T), h_T [N, D] fp32 or None when
     output_final_state is False."""
-    lib = kda.load_library()
     dev = _device_of("x", x)
-    _need("x", x, dev)
-    _need("log_alpha", log_alpha, dev, x.shape)
+    shape = x.shape
+    _need("x", x, dev, shape, x.dtype)
+    _need("log_alpha", log_alpha, dev, shape, log_alpha.dtype)
     B, T, D, N, nseq = _glr_sizes(x, cu_seqlens, dev)
     f32 = torch.float32
     if h0 is not None:
         _need("h0", h0, dev, (N, D), f32)
-    io, gt = kda._dtype_code(x), kda._dtype_code(log_alpha)
+    io, gt = _code(x), _code(log_alpha)
     if h is None:
         h = torch.empty_like(x)
     else:
@@ -151,20 +158,17 @@ def kda_glr_fwd(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_T=None, out
         _need("h_T", h_T, dev, (N, D), f32)
     elif output_final_state:
         h_T = torch.empty((N, D), dtype=f32, device=dev)
-    ws, wsb = _glr_workspace(lib, B, T, D, nseq, io, workspace, dev)
-    with _on(dev):
-        rc = lib.kda_glr_fwd(_p(x), _p(log_alpha), _p(h0), _p(cu_seqlens), nseq, _p(h), _p(h_T), B, T, D, io, gt,
-                             _p(ws), wsb, _stream(dev))
-    _check(rc, "kda_glr_fwd")
+    ws, wsb = _glr_workspace(B, T, D, nseq, io, workspace, dev)
+    _launch(dev, "kda_glr_fwd", _p(x), _p(log_alpha), _p(h0), _p(cu_seqlens), nseq, _p(h), _p(h_T), B, T, D, io, gt,
+            _p(ws), wsb)
     return h, h_T
 
 
 def _glr_bwd(name, log_alpha, h, scales, grad_h, h0, grad_hT, cu_seqlens, want_grad_h0, workspace):
-    lib = kda.load_library()
     dev = _device_of("grad_h", grad_h)
     f32 = torch.float32
-    _need("grad_h", grad_h, dev)
-    _need("log_alpha", log_alpha, dev, grad_h.shape)
+    _need("grad_h", grad_h, dev, grad_h.shape, grad_h.dtype)
+    _need("log_alpha", log_alpha, dev, grad_h.shape, log_alpha.dtype)
     B, T, D, N, nseq = _glr_sizes(grad_h, cu_seqlens, dev)
     if scales is None:
         _need("h", h, dev, grad_h.shape, grad_h.dtype)
@@ -174,15 +178,13 @@ def _glr_bwd(name, log_alpha, h, scales, grad_h, h0, grad_hT, cu_seqlens, want_g
     for n, t in (("h0", h0), ("grad_hT", grad_hT)):
         if t is not None:
             _need(n, t, dev, (N, D), f32)
-    io, gt = kda._dtype_code(grad_h), kda._dtype_code(log_alpha)
+    io, gt = _code(grad_h), _code(log_alpha)
     dx, dla = torch.empty_like(grad_h), torch.empty_like(log_alpha)
     dh0 = torch.empty((N, D), dtype=f32, device=dev) if want_grad_h0 else None
-    ws, wsb = _glr_workspace(lib, B, T, D, nseq, io, workspace, dev)
+    ws, wsb = _glr_workspace(B, T, D, nseq, io, workspace, dev)
     saved = (_p(h),) if scales is None else (_p(h), _p(scales))
-    with _on(dev):
-        rc = getattr(lib, name)(_p(log_alpha), *saved, _p(h0), _p(cu_seqlens), nseq, _p(grad_h), _p(grad_hT), _p(dx),
-                                _p(dla), _p(dh0), B, T, D, io, gt, _p(ws), wsb, _stream(dev))
-    _check(rc, name)
+    _launch(dev, name, _p(log_alpha), *saved, _p(h0), _p(cu_seqlens), nseq, _p(grad_h), _p(grad_hT), _p(dx), _p(dla),
+            _p(dh0), B, T, D, io, gt, _p(ws), wsb)
     return dx, dla, dh0
 
 
@@ -201,22 +203,20 @@ def kda_glr_bwd_act8(log_alpha, h_codes, h_scales, grad_h, h0=None, grad_hT=None
 
 def kda_glr_step(x, log_alpha, S, h=None):
     """One token of kda_glr_fwd: x, log_alpha [B, D]; S [B, D] fp32, updated in place.  Returns h."""
-    lib = kda.load_library()
     dev = _device_of("x", x)
     if x.dim() != 2:
         raise ValueError("x must be [B, D], not %s" % (tuple(x.shape),))
-    _need("x", x, dev)
-    _need("log_alpha", log_alpha, dev, x.shape)
-    _need("S", S, dev, x.shape, torch.float32)
+    shape, io = x.shape, x.dtype
+    _need("x", x, dev, shape, io)
+    _need("log_alpha", log_alpha, dev, shape, log_alpha.dtype)
+    _need("S", S, dev, shape, torch.float32)
     if h is None:
         h = torch.empty_like(x)
     else:
-        _need("h", h, dev, x.shape, x.dtype)
-    B, D = x.shape
-    with _on(dev):
-        rc = lib.kda_glr_step(_p(x), _p(log_alpha), _p(S), _p(h), B, D, kda._dtype_code(x),
-                              kda._dtype_code(log_alpha), _stream(dev))
-    _check(rc, "kda_glr_step")
+        _need("h", h, dev, shape, io)
+    B, D = shape
+    _launch(dev, "kda_glr_step", x.data_ptr(), log_alpha.data_ptr(), S.data_ptr(), h.data_ptr(), B, D, _code(x),
+            _code(log_alpha))
     return h
 
 
@@ -231,40 +231,35 @@ def _rows_cols(name, t):
 def kda_act8_pack(x, *, codes=None, scales=None):
     """x [..., d] in 8 bits: (codes int8 [..., d], scales fp32 [..., ceil(d / 128)]),
     one scale for each 128 consecutive values of the last axis."""
-    lib = kda.load_library()
     dev = _device_of("x", x)
-    _need("x", x, dev)
+    _need("x", x, dev, x.shape, x.dtype)
     rows, cols = _rows_cols("x", x)
-    sshape = tuple(x.shape[:-1]) + (_blocks(cols),)
+    sshape = (*x.shape[:-1], _blocks(cols))
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        codes = torch.empty_like(x, dtype=torch.int8)
     else:
         _need("codes", codes, dev, x.shape, torch.int8)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+        scales = x.new_empty(sshape, dtype=torch.float32)
     else:
         _need("scales", scales, dev, sshape, torch.float32)
-    with _on(dev):
-        rc = lib.kda_act8_pack(_p(x), _p(codes), _p(scales), rows, cols, kda._dtype_code(x), _stream(dev))
-    _check(rc, "kda_act8_pack")
+    _launch(dev, "kda_act8_pack", x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, cols, _code(x))
     return codes, scales
 
 
 def kda_act8_unpack(codes, scales, dtype=None, *, out=None):
     """The values that codes and scales (kda_act8_pack) stand for, in dtype
     (bfloat16 unless given)."""
-    lib = kda.load_library()
     dev = _device_of("codes", codes)
-    _need("codes", codes, dev, dtype=torch.int8)
+    shape = codes.shape
+    _need("codes", codes, dev, shape, torch.int8)
     rows, cols = _rows_cols("codes", codes)
-    _need("scales", scales, dev, tuple(codes.shape[:-1]) + (_blocks(cols),), torch.float32)
+    _need("scales", scales, dev, (*shape[:-1], _blocks(cols)), torch.float32)
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype or torch.bfloat16, device=dev)
+        out = torch.empty_like(codes, dtype=dtype or torch.bfloat16)
     else:
-        _need("out", out, dev, codes.shape, dtype)
-    with _on(dev):
-        rc = lib.kda_act8_unpack(_p(codes), _p(scales), _p(out), rows, cols, kda._dtype_code(out), _stream(dev))
-    _check(rc, "kda_act8_unpack")
+        _need("out", out, dev, shape, dtype)
+    _launch(dev, "kda_act8_unpack", codes.data_ptr(), scales.data_ptr(), out.data_ptr(), rows, cols, _code(out))
     return out
 
 
@@ -273,7 +268,6 @@ def kda_chunk_bwd_act8_workspace_size(B, T, H, d_k, d_v, num_seqs=0, io_dtype=1)
 
 
 def _chunk_bwd_act8(name, q8, k8, v8, log_alpha, beta, grad_o, h0, grad_hT, cu_seqlens, want_grad_h0, workspace):
-    lib = kda.load_library()
     gdn = name == "kda_gdn_chunk_bwd_act8"
     dev = _device_of("grad_o", grad_o)
     f32, i8 = torch.float32, torch.int8
@@ -298,23 +292,20 @@ def _chunk_bwd_act8(name, q8, k8, v8, log_alpha, beta, grad_o, h0, grad_hT, cu_s
     for n, t in (("h0", h0), ("grad_hT", grad_hT)):
         if t is not None:
             _need(n, t, dev, (N, H, dk, dv), f32)
-    io, gt = kda._dtype_code(grad_o), kda._dtype_code(beta)
+    io, gt = _code(grad_o), _code(beta)
     new = lambda d: torch.empty(lead + (d,), dtype=grad_o.dtype, device=dev)  # noqa: E731
     dq, dk_, dv_ = new(dk), new(dk), new(dv)
     dla = None if log_alpha is None else torch.empty_like(log_alpha)
     db = torch.empty_like(beta)
     dh0 = torch.empty((N, H, dk, dv), dtype=f32, device=dev) if want_grad_h0 else None
     if workspace is None:
-        need = lib.kda_chunk_bwd_act8_workspace_size(B, T, H, dk, dv, nseq, io)
+        need = kda.load_library().kda_chunk_bwd_act8_workspace_size(B, T, H, dk, dv, nseq, io)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     else:
         _need("workspace", workspace, dev)
-    with _on(dev):
-        rc = getattr(lib, name)(_p(q8[0]), _p(q8[1]), _p(k8[0]), _p(k8[1]), _p(v8[0]), _p(v8[1]), _p(log_alpha),
-                                _p(beta), _p(h0), _p(cu_seqlens), nseq, _p(grad_o), _p(grad_hT), _p(dq), _p(dk_),
-                                _p(dv_), _p(dla), _p(db), _p(dh0), B, T, H, dk, dv, io, gt, _p(workspace),
-                                workspace.numel() * workspace.element_size(), _stream(dev))
-    _check(rc, name)
+    _launch(dev, name, _p(q8[0]), _p(q8[1]), _p(k8[0]), _p(k8[1]), _p(v8[0]), _p(v8[1]), _p(log_alpha), _p(beta),
+            _p(h0), _p(cu_seqlens), nseq, _p(grad_o), _p(grad_hT), _p(dq), _p(dk_), _p(dv_), _p(dla), _p(db), _p(dh0),
+            B, T, H, dk, dv, io, gt, _p(workspace), workspace.numel() * workspace.element_size())
     return dq, dk_, dv_, dla, db, dh0
 
 
@@ -335,14 +326,13 @@ def kda_gdn_chunk_bwd_act8(q8, k8, v8, log_alpha, beta, grad_o, h0=None, grad_hT
 
 # ------------------------------------------------------------------- RMS norm
 def _norm_fwd(name, x, weight, residual, eps, y, codes, scales, r, want_rstd):
-    lib = kda.load_library()
     dev = _device_of("x", x)
     f32 = torch.float32
-    _need("x", x, dev)
+    _need("x", x, dev, x.shape, x.dtype)
     rows, cols = _rows_cols("x", x)
     if weight is not None:
-        _need("weight", weight, dev, (cols,))
-    io, wt = kda._dtype_code(x), kda._dtype_code(x if weight is None else weight)
+        _need("weight", weight, dev, (cols,), weight.dtype)
+    io, wt = _code(x), _code(x if weight is None else weight)
     if residual is None:
         if r is not None:
             raise ValueError("r is the sum with a residual: there is none")
@@ -352,7 +342,7 @@ def _norm_fwd(name, x, weight, residual, eps, y, codes, scales, r, want_rstd):
             r = torch.empty_like(x)
         else:
             _need("r", r, dev, x.shape, x.dtype)
-    rstd = torch.empty(x.shape[:-1], dtype=f32, device=dev) if want_rstd else None
+    rstd = x.new_empty(x.shape[:-1], dtype=f32) if want_rstd else None
     if name == "kda_rmsnorm_fwd":
         if y is None:
             y = torch.empty_like(x)
@@ -360,20 +350,17 @@ def _norm_fwd(name, x, weight, residual, eps, y, codes, scales, r, want_rstd):
             _need("y", y, dev, x.shape, x.dtype)
         out = (_p(y),)
     else:
-        sshape = tuple(x.shape[:-1]) + (_blocks(cols),)
+        sshape = (*x.shape[:-1], _blocks(cols))
         if codes is None:
-            codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+            codes = torch.empty_like(x, dtype=torch.int8)
         else:
             _need("codes", codes, dev, x.shape, torch.int8)
         if scales is None:
-            scales = torch.empty(sshape, dtype=f32, device=dev)
+            scales = x.new_empty(sshape, dtype=f32)
         else:
             _need("scales", scales, dev, sshape, f32)
         out = (_p(codes), _p(scales))
-    with _on(dev):
-        rc = getattr(lib, name)(_p(x), _p(residual), _p(weight), *out, _p(r), _p(rstd), rows, cols, eps, io, wt,
-                                _stream(dev))
-    _check(rc, name)
+    _launch(dev, name, _p(x), _p(residual), _p(weight), *out, _p(r), _p(rstd), rows, cols, eps, io, wt)
     r = x if residual is None else r
     return (y, r, rstd) if name == "kda_rmsnorm_fwd" else (codes, scales, r, rstd)
 
@@ -398,10 +385,9 @@ def kda_rmsnorm_bwd_workspace_size(rows, cols) -> int:
 
 
 def _norm_bwd(name, r, scales, weight, rstd, grad_y, grad_r, want_grad_weight, grad_x, workspace):
-    lib = kda.load_library()
     dev = _device_of("grad_y", grad_y)
     f32 = torch.float32
-    _need("grad_y", grad_y, dev)
+    _need("grad_y", grad_y, dev, grad_y.shape, grad_y.dtype)
     rows, cols = _rows_cols("grad_y", grad_y)
     if scales is None:
         _need("r", r, dev, grad_y.shape, grad_y.dtype)
@@ -412,27 +398,25 @@ def _norm_bwd(name, r, scales, weight, rstd, grad_y, grad_r, want_grad_weight, g
         saved = (_p(r), _p(scales))
     _need("rstd", rstd, dev, grad_y.shape[:-1], f32)
     if weight is not None:
-        _need("weight", weight, dev, (cols,))
+        _need("weight", weight, dev, (cols,), weight.dtype)
     if grad_r is not None:
         _need("grad_r", grad_r, dev, grad_y.shape, grad_y.dtype)
-    io, wt = kda._dtype_code(grad_y), kda._dtype_code(grad_y if weight is None else weight)
+    io, wt = _code(grad_y), _code(grad_y if weight is None else weight)
     if grad_x is None:
         grad_x = torch.empty_like(grad_y)
     else:
         _need("grad_x", grad_x, dev, grad_y.shape, grad_y.dtype)
     gw = None
     if want_grad_weight:
-        gw = torch.empty((cols,), dtype=grad_y.dtype if weight is None else weight.dtype, device=dev)
+        gw = grad_y.new_empty((cols,)) if weight is None else torch.empty_like(weight)
         if workspace is None:
-            need = lib.kda_rmsnorm_bwd_workspace_size(rows, cols)
+            need = kda.load_library().kda_rmsnorm_bwd_workspace_size(rows, cols)
             workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if workspace is not None:
         _need("workspace", workspace, dev)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(dev):
-        rc = getattr(lib, name)(*saved, _p(weight), _p(rstd), _p(grad_y), _p(grad_r), _p(grad_x), _p(gw), rows, cols,
-                                io, wt, _p(workspace), wsb, _stream(dev))
-    _check(rc, name)
+    _launch(dev, name, *saved, _p(weight), _p(rstd), _p(grad_y), _p(grad_r), _p(grad_x), _p(gw), rows, cols, io, wt,
+            _p(workspace), wsb)
     return grad_x, gw
 
 
