@@ -254,24 +254,24 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const void *__restri
 }
 
 // The sum of the partial rows: 32 columns a workgroup, 8 threads deep in columns
-// and 32 in rows, each with eight rows' loads in flight (it is the latency of these
+// and 32 in rows, each with sixteen rows' loads in flight (it is the latency of these
 // that it takes: 512 partial rows of 128 columns in 11 us one at a time).
 __global__ __launch_bounds__(kThreads) void norm_join_kernel(const float *__restrict__ partial, int32_t partials,
                                                              int32_t cols, void *gw, int32_t w_bf16) {
     __shared__ float sh[32][33];
     const int cg = threadIdx.x % 8, rg = threadIdx.x / 8, c0 = blockIdx.x * 32 + cg * 4;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int row = rg; row < partials; row += 32 * 8) {
-        float v[8][4];
+    for (int row = rg; row < partials; row += 32 * 16) {
+        float v[16][4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool there = row + 32 * k < partials && c0 + e < cols;
                 v[k][e] = there ? partial[(int64_t)(row + 32 * k) * cols + c0 + e] : 0.f;
             }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] += v[k][e];
     }
