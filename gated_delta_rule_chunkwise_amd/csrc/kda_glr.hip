@@ -207,12 +207,12 @@ template <typename IO, typename GT, int MODE, int VEC>
 __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, GT, MODE, VEC> &row, const float *hs,
                                               int64_t t0, int c0, int skip, float (&s)[VEC]) {
     constexpr int R = span_tokens<IO, GT, MODE, VEC>();
-    IO *out = static_cast<IO *>(p.out);
-    GT *dla = static_cast<GT *>(p.dla);
+    IO *out = static_cast<IO *>(p.out) + t0 * p.D + c0;
+    GT *dla = static_cast<GT *>(p.dla) + t0 * p.D + c0;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int i = MODE == kFwd ? k : R - 1 - k;
-        const int64_t at = (t0 + i) * p.D + c0;
+        const int64_t to = (int64_t)i * p.D;   // the same for all lanes
         float o[VEC], d[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -231,11 +231,11 @@ __device__ __forceinline__ void finish_inside(const GlrParams &p, const Row<IO, 
         if (skip) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                if (e >= skip) out[at + e] = from_f32<IO>(o[e]);
+                if (e >= skip) out[to + e] = from_f32<IO>(o[e]);
         } else {
-            store_vec<IO, VEC>(out + at, o);
+            store_vec<IO, VEC>(out + to, o);
         }
-        if constexpr (MODE != kFwd) store_vec<GT, VEC>(dla + at, d);
+        if constexpr (MODE != kFwd) store_vec<GT, VEC>(dla + to, d);
     }
 }
 
@@ -305,8 +305,8 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
     constexpr int R = span_tokens<IO, GT, MODE, VEC>();
     const uint32_t starts = MODE == kFwd ? at.first : at.last, ends = MODE == kFwd ? at.last : at.first;
     int64_t n = MODE == kFwd ? at.n_first : at.n_last;
-    IO *out = static_cast<IO *>(p.out);
-    GT *dla = static_cast<GT *>(p.dla);
+    IO *out = static_cast<IO *>(p.out) + t0 * p.D + c0;
+    GT *dla = static_cast<GT *>(p.dla) + t0 * p.D + c0;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int i = MODE == kFwd ? k : R - 1 - k;
@@ -323,7 +323,7 @@ __device__ __forceinline__ void finish_border(const GlrParams &p, const Seqs &q,
                 load_f32<VEC>(src + n * p.D + c0, s);
             }
         }
-        const int64_t to = (t0 + i) * p.D + c0;
+        const int64_t to = (int64_t)i * p.D;
         float o[VEC], d[VEC], h[VEC];
         if constexpr (MODE != kFwd) {
 #pragma unroll
