@@ -496,12 +496,15 @@ def gated_linear_recurrence(x, log_alpha, h0=None, cu_seqlens=None, *, act8=Fals
     """kda_glr_fwd with autograd: returns (h, h_T), and gradients flow to x,
     log_alpha and h0 through kda_glr_bwd.  With act8 the forward keeps h for the
     backward in 8 bits (about half of bf16's memory); dlog_alpha is then taken at
-    those values, dx and dh0 do not depend on them."""
+    those values, dx and dh0 do not depend on them.  Under graph capture call
+    kda_glr_fwd and kda_glr_bwd instead: torch may not run a captured backward while
+    an eager graph of the same leaves lives."""
     return _function("glr").apply(x, log_alpha, h0, cu_seqlens, act8)
 
 
 def rms_norm(x, weight=None, residual=None, eps=1e-6, *, act8=False):
     """kda_rmsnorm_fwd with autograd: returns y, or (y, r) with a residual, r = x +
     residual being the new stream.  Gradients flow to x, weight and residual.  With
-    act8 the forward keeps r for the backward in 8 bits."""
+    act8 the forward keeps r for the backward in 8 bits.  Under graph capture call
+    kda_rmsnorm_fwd and kda_rmsnorm_bwd instead, as for gated_linear_recurrence."""
     return _function("norm").apply(x, weight, residual, eps, act8)

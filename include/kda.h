@@ -471,8 +471,8 @@ kda_status_t kda_gdn_chunk_bwd(const void *q, const void *k, const void *v, cons
 /*
  * Bytes of device workspace kda_glr_fwd, kda_glr_bwd and kda_glr_bwd_act8 need
  * (0 if none, or for invalid arguments).  A batch of few tokens (one time tile)
- * needs none; others keep one 8-byte map per time tile and channel (with
- * many channels 1/16 byte per token and channel in bf16, 1/8 in fp32).  The size
+ * needs none; others keep one 8-byte map per time tile and channel (with many
+ * channels 1/8 byte per token and channel, sized for the shortest tile).  The size
  * depends only on the arguments.
  */
 size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs, int32_t io_dtype);
