@@ -455,6 +455,7 @@ def _function(name):
                 return h, h_T
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, grad_h, grad_hT):
                 log_alpha, h0, cu_seqlens, h, scales = ctx.saved_tensors
                 if grad_h is None and grad_hT is None:
@@ -478,6 +479,7 @@ def _function(name):
                 return (y, r) if ctx.with_residual else y
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, grad_y, grad_r=None):
                 weight, rstd, r, scales = ctx.saved_tensors
                 if grad_y is None:   # only the stream's sum was used

@@ -761,3 +761,15 @@ def test_binding_refusals():
         with pytest.raises(kda.KDAError) as e:
             kda.kda_glr_fwd(big, big, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
         assert e.value.code == kda.KDA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("act8", [False, True])
+def test_second_derivatives_are_refused(act8):
+    """The gradients are the library's own and have no formula of a second order:
+    asking for one is an error, not a gradient that leaves a part out."""
+    x = randn((1, 5, 3), 1).to(DEV).requires_grad_()
+    g = gate((1, 5, 3), 2).to(DEV)
+    for y in (kda.gated_linear_recurrence(x, g, act8=act8)[0], kda.rms_norm(x, act8=act8)):
+        (dx,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            dx.sum().backward()
