@@ -24,9 +24,10 @@
 // are handed out by a ticket in order of time, one for each channel tile, so a tile
 // only ever waits for tiles that are already running: the wait ends.
 //
-// Measured (copies on this card: 6.2 TB/s): bf16 forward of 65536 x 4096 in 306 us
-// (5.3 TB/s), backward of 65536 x 2048 in 242 us (5.5 TB/s), from 8-bit h over a
-// packed batch of 139,000 tokens x 2048 in 541 us (4.8 TB/s); without the waits for
+// Measured (copies on this card: 6.2 TB/s): bf16 forward of 65536 x 4096 in 314 us
+// (5.1 TB/s), backward of 65536 x 2048 in 250 us (5.4 TB/s), from 8-bit h over a
+// packed batch of 139,000 tokens x 2048 in 557 us (4.6 TB/s), 2% of each for factors
+// that tell a reset from one that is out of range; without the waits for
 // other tiles the first is 8% shorter, the rest of the way is the pieces of 512 bytes
 // of a token that a wave takes.  Smaller tiles (64 tokens) and one workgroup a CU
 // (256 tokens) took 20% and 10% longer.  Rows of an odd number of channels share
@@ -113,6 +114,14 @@ template <int VEC> __device__ __forceinline__ void load_f32(const float *p, floa
 
 // a s, where a = 0 drops s whatever it is (a reset).
 __device__ __forceinline__ float decayed(float a, float s) { return a == 0.f ? 0.f : a * s; }
+// The factor of a span or a tile is 0 only where one of its tokens is a reset;
+// otherwise it ends at the smallest positive number, whose product with a state is as
+// good as 0, but for an infinity or a NaN, which stay what they are.  Factors are not
+// negative: their bits are in their order.
+__device__ __forceinline__ uint32_t bits_of(float a) { return __builtin_bit_cast(uint32_t, a); }
+__device__ __forceinline__ float not_below(float a, uint32_t least) {
+    return __builtin_bit_cast(float, max(bits_of(a), least));
+}
 
 struct GlrParams {
     const void *x, *la, *h;
@@ -372,7 +381,7 @@ template <int VEC> struct alignas(VEC * 8) Map {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             b[e] = decayed(m.a[e], b[e]) + m.b[e];
-            a[e] *= m.a[e];
+            a[e] = not_below(a[e] * m.a[e], min(min(bits_of(a[e]), bits_of(m.a[e])), 1u));
         }
     }
     // then m[0], m[stride], .., n of them: loads in batches, so that their latency
@@ -461,14 +470,25 @@ __global__ __launch_bounds__(kNT, 4) void glr_kernel(const GlrParams p) {
         }
     }
 
-    float L[VEC];
+    float L[VEC];   // the logarithm of the span's factor
     Map<VEC> own;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) L[e] = 0.f, own.b[e] = 0.f;
     if (!plain) compose_border<IO, GT, MODE, VEC>(p, q, at, row, t0, nv, c0, L, own.b);
     else if (chan) compose_inside<IO, GT, MODE, VEC>(row, L, own.b);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) own.a[e] = __expf(L[e]);
+    for (int e = 0; e < VEC; ++e) {
+        own.a[e] = __expf(L[e]);
+        // out of range, and not by a border or a gate of -inf: seldom, so that only
+        // then the gates are asked whether one of them is a reset
+        if (own.a[e] == 0.f && L[e] > -__builtin_inff()) {
+            float least = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (i < nv) least = fminf(least, raw_at<VEC>(row.la[i], e));
+            own.a[e] = not_below(0.f, __expf(least) == 0.f ? 0 : 1);
+        }
+    }
     sm.row[tid] = own;
     if constexpr (MODE == kBwd8) {
 #pragma unroll

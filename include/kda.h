@@ -501,8 +501,9 @@ size_t kda_glr_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
  *
  * Numerics: states and every product are fp32; h is rounded to io_dtype with
  * round-to-nearest-even.  Deterministic: the same inputs give bitwise identical
- * outputs.  The products of decays over a span of tokens are formed in fp32; a
- * span whose product underflows counts as a reset.  alpha is rounded to fp32: under
+ * outputs.  The products of decays over a span of tokens are formed in fp32; one
+ * that is out of range leaves nothing of a finite state, and an infinity or a NaN
+ * as it is: these end at a reset only.  alpha is rounded to fp32: under
  * a gate that stays within 1e-4 of 1 the state's relative error grows to about
  * 6e-8 / (1 - alpha).  Tokens behind cu_seqlens[N] are neither read nor written.
  */

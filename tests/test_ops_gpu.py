@@ -773,3 +773,37 @@ def test_second_derivatives_are_refused(act8):
         (dx,) = torch.autograd.grad((y * y).sum(), x, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             dx.sum().backward()
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("D", [3, 64, 130])
+def test_glr_infinities_last_until_a_reset(D, io, act8):
+    """An infinity or a NaN stays in the state however far its factor has decayed,
+    as in the formula (alpha > 0 times infinity), and ends at a reset; the other
+    channels do not see it."""
+    T, reset = 5000, 4000
+    inf = float("inf")
+    x, g = randn((T, D), 1, io).to(DEV), gate((T, D), 2, io, "uniform").to(DEV)
+    g[:, 2] = -6.0                      # decays within a span
+    g[reset] = -inf
+    clean, _ = kda.kda_glr_fwd(x, g)
+    y = x.clone()
+    y[7, 0], y[9, 1], y[11, 2] = inf, float("nan"), -inf
+    h, hT = kda.kda_glr_fwd(y, g)
+    assert (h[7:reset, 0] == inf).all() and h[9:reset, 1].isnan().all() and (h[11:reset, 2] == -inf).all()
+    for c, t in ((0, 7), (1, 9), (2, 11)):
+        assert torch.equal(h[:t, c], clean[:t, c])
+    assert torch.equal(h[reset:], clean[reset:]) and torch.equal(h[:, 3:], clean[:, 3:])
+    assert hT.isfinite().all()
+
+    saved = kda.kda_act8_pack(clean) if act8 else (clean,)
+    bwd = kda.kda_glr_bwd_act8 if act8 else kda.kda_glr_bwd
+    want, _, _ = bwd(g, *saved, x)
+    y = x.clone()
+    y[T - 7, 0], y[reset - 9, 1], y[reset - 11, 2] = inf, float("nan"), -inf
+    dx, _, dh0 = bwd(g, *saved, y)
+    assert (dx[reset:T - 6, 0] == inf).all() and torch.equal(dx[:reset, 0], want[:reset, 0])
+    assert dx[:reset - 8, 1].isnan().all() and (dx[:reset - 10, 2] == -inf).all()
+    assert torch.equal(dx[reset:, 1:], want[reset:, 1:]) and torch.equal(dx[:, 3:], want[:, 3:])
+    assert dh0[0, 1].isnan() and dh0[0, 2] == -inf and dh0[0, 0].isfinite()
